@@ -41,8 +41,8 @@
  *       too small, unsupported shape), EP_ERR_HIP (a HIP runtime call failed).
  *     Data errors found on the device never force a sync: they are reported
  *     in the per-plan status words (EP_STATUS_*).
- *   - Integer work throughout; results do not depend on scheduling (no
- *     order-dependent atomics), so every output is bit-reproducible.
+ *   - The balancing path is integer work throughout; no call's results depend on
+ *     scheduling (no order-dependent atomics), so every output is bit-reproducible.
  */
 #ifndef EP_BALANCE_H
 #define EP_BALANCE_H
@@ -372,6 +372,220 @@ int ep_route_noalloc(const int32_t *topk_ids, int64_t pairs_per_plan, int32_t nu
                      const ep_layout_t *layout, int32_t *load, uint32_t *status, int32_t *phy2log,
                      int32_t *phy_quota, int32_t *logcnt, int32_t *log2phy, int32_t *steps,
                      int32_t *phys_ids, ep_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The layer around the balancer: the gate that makes the expert IDs, the
+ * experts' products over the dispatch order, the layer for a few tokens and
+ * the optimizer step on the folded gradients.  The conventions above hold:
+ * device pointers of the caller, no allocation, enqueue only, results that do
+ * not depend on scheduling.
+ * ------------------------------------------------------------------------- */
+enum {
+    EP_DTYPE_F32 = 0,
+    EP_DTYPE_BF16 = 1,
+    EP_DTYPE_FP8 = 2, /* OCP e4m3 with power-of-two block scales, see ep_quant_rows */
+};
+
+/*
+ * Gate: the top-k experts of every token and their weights.
+ *   score  s_e = logit_e + bias_e in fp32; NaN counts as -inf, and -inf (an
+ *          expert switched off, a padded token) is never chosen
+ *   groups num_groups > 1: experts form equal consecutive groups, a group's
+ *          score is its best s, and only the topk_groups best groups stay
+ *          (equal ones: lowest group)
+ *   chosen the top_k largest s, in descending order (equal ones: lowest
+ *          expert); where fewer are left, ID -1 (padding to the calls above)
+ *          and weight 0
+ *   weight w_j = scale * exp(logit_j) / sum_i exp(logit_i) over the chosen
+ *          (without the bias), computed from the largest one on
+ * num_experts <= 1024, top_k <= 16, num_groups <= 16 and dividing num_experts.
+ */
+typedef struct ep_gate {
+    int32_t num_experts, top_k;
+    int32_t num_groups, topk_groups; /* 1, 1: no group limit */
+    int32_t logits_dtype;            /* EP_DTYPE_F32 or EP_DTYPE_BF16 */
+    float scale;                     /* finite */
+    const float *bias;               /* device [E] or NULL; moves the choice, not the weights */
+} ep_gate_t;
+
+/*
+ *   logits   device [T][stride], stride >= E elements
+ *   ids      device int32 [T][k], weights device float [T][k] (written)
+ */
+int ep_gate_topk(const void *logits, int64_t stride, int64_t num_tokens, const ep_gate_t *gate, int32_t *ids,
+                 float *weights, ep_stream_t stream);
+
+/*
+ * Gradient of the weights with respect to the logits:
+ *   dl_j = w_j (g_j - sum_i w_i g_i / scale) at the chosen experts, 0 elsewhere.
+ * gate: num_experts, top_k, scale and logits_dtype (of grad_logits) are used.
+ *   ids, weights  as ep_gate_topk wrote them; grad_weights device float [T][k]
+ *   grad_logits   device [T][E], every element written
+ */
+int ep_gate_topk_backward(const int32_t *ids, const float *weights, const float *grad_weights, int64_t num_tokens,
+                          const ep_gate_t *gate, void *grad_logits, ep_stream_t stream);
+
+/*
+ * 8-bit floating point with a scale for each block of 128: values are OCP e4m3
+ * bytes, and a block's scale is the byte c, standing for 2^(c - 127), the
+ * smallest power of two that brings the block's largest magnitude to 448 at
+ * most.  Rounding is to nearest, ties to even; NaN and infinities become NaN.
+ *
+ * ep_quant_rows: blocks of 128 columns of one row, for activations.
+ *   x      device [rows][stride] fp32 or bf16
+ *   q      device bytes [rows][cols up to a multiple of 128], zeros past cols, 16-byte aligned
+ *   scale  device bytes [rows][ep_scale_stride(cols)] (the number of blocks up
+ *          to a multiple of 4; the bytes past the blocks are 127), 4-byte aligned
+ * ep_swiglu_quant: the same for silu(g) * u, where a bf16 row of 2 * inter
+ * values holds g and then u.
+ * ep_quant_blocks: blocks of 128 rows x 128 columns, for weights.
+ *   w      device [groups][rows][cols], group_stride elements between groups
+ *   q      bytes [groups][rows][cols up to 128], scale bytes
+ *          [groups][row blocks][column blocks]; with transpose != 0 those of
+ *          the transposed matrices: q [groups][cols][rows up to 128], scale
+ *          [groups][column blocks][row blocks], the same values
+ */
+int64_t ep_scale_stride(int64_t cols);
+int ep_quant_rows(const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride, uint8_t *q,
+                  uint8_t *scale, ep_stream_t stream);
+int ep_swiglu_quant(const void *gate_up, int64_t rows, int64_t inter, uint8_t *q, uint8_t *scale,
+                    ep_stream_t stream);
+int ep_quant_blocks(const void *w, int32_t dtype, int32_t groups, int64_t group_stride, int64_t rows, int64_t cols,
+                    int32_t transpose, uint8_t *q, uint8_t *scale, ep_stream_t stream);
+
+/* The matrices of a set of experts; `stride` bytes and `scale_stride` bytes from
+ * one expert to the next, so that a matrix may be a part of a packed expert row.
+ * data 16-byte aligned, stride a multiple of 16.  scale: NULL unless the data
+ * are EP_DTYPE_FP8. */
+typedef struct ep_matrix {
+    const void *data;
+    const uint8_t *scale;
+    int64_t stride, scale_stride;
+} ep_matrix_t;
+
+/*
+ * Grouped product: y[i] = w_g x[r(i)] for the output rows i of group g, the
+ * consecutive rows offsets[g] .. offsets[g + 1] - 1.  Offsets outside [0, m] or
+ * out of order are brought into range and order; rows from offsets[groups] on
+ * become 0.
+ *   x, x_scale  as ep_quant_rows writes them: k columns, x_rows rows
+ *   rows        device int32 [m] or NULL: r(i) = rows[i] / rows_div (the pair
+ *               that a dispatch position serves, rows_div = top-k); a negative
+ *               or too large row gives y[i] = 0.  NULL: r(i) = i, x_rows >= m
+ *   offsets     device int32 [groups + 1], or NULL with one group: all rows
+ *   w           [groups][n][k], as ep_quant_blocks writes them
+ *   layout      NULL, or the layout whose physical slots are the groups: then w
+ *               holds the native experts [E] and slot_w the spare slots [S]
+ *               (the slot buffer), and slot_offsets of ep_dispatch_layout are
+ *               the offsets
+ *   y           device bf16 [m][n], every element written
+ * The input gradient is the same call on the quantised output gradient with
+ * weights from ep_quant_blocks(transpose = 1).  m < 2^31 - 1024.
+ */
+typedef struct ep_grouped_matmul {
+    const void *x;
+    const uint8_t *x_scale;
+    int64_t x_rows;
+    const int32_t *rows;
+    int32_t rows_div;
+    int32_t groups;
+    const int32_t *offsets;
+    int64_t m, n, k;
+    ep_matrix_t w, slot_w;
+    const ep_layout_t *layout;
+    void *y;
+} ep_grouped_matmul_t;
+int ep_grouped_matmul(const ep_grouped_matmul_t *p, ep_stream_t stream);
+
+/*
+ * Weight gradient of the grouped product: out_g[n][k] = sum over the rows i of
+ * group g of dy[i][n] x[i][k], fp32, every element written (0 for an empty
+ * group).  dy, x: device bf16 [m][dy_stride], [m][x_stride] (elements).
+ * groups, offsets as above.  With a layout the physical slots' gradients go to
+ * out [E] (native) and slot_out [S], the two inputs of ep_replica_grad_reduce.
+ * out_stride, slot_out_stride: floats from one group to the next.
+ */
+typedef struct ep_grouped_wgrad {
+    const void *dy, *x;
+    int64_t dy_stride, x_stride;
+    int64_t m, n, k;
+    int32_t groups;
+    const int32_t *offsets;
+    const ep_layout_t *layout;
+    float *out, *slot_out;
+    int64_t out_stride, slot_out_stride;
+} ep_grouped_wgrad_t;
+int ep_grouped_wgrad(const ep_grouped_wgrad_t *p, ep_stream_t stream);
+
+/*
+ * Combine: out_t = sum_j weights[t][j] * y[pos[t][j]] in fp32, j ascending,
+ * rounded to bf16 once.  pos: device int32 [T][k] (dispatch_pos of
+ * ep_dispatch_layout); positions outside [0, rows) give nothing.  y: bf16
+ * [rows][hidden], out: bf16 [T][hidden].
+ */
+int ep_moe_combine(const void *y, int64_t rows, const int32_t *pos, const float *weights, int64_t num_tokens,
+                   int32_t top_k, int64_t hidden, void *out, ep_stream_t stream);
+
+/*
+ * A whole mixture-of-experts layer for up to EP_MAX_FEW_TOKENS tokens:
+ *   ids, w  as ep_gate_topk
+ *   out_t = sum_j w_tj down_e (silu(gate_e x_t) * (up_e x_t)),  e = ids_tj >= 0
+ * summed in fp32 and rounded to bf16 once.  Every distinct expert's weights are
+ * read once.
+ *   x        device bf16 [T][x_stride], 16-byte aligned, x_stride a multiple of 8
+ *   logits   as for ep_gate_topk
+ *   experts  bf16 matrices gate, up [E][inter][hidden], down [E][hidden][inter],
+ *            or the same in 8 bits as ep_quant_blocks writes them (x stays bf16;
+ *            bytes past a row's columns must be 0); hidden and inter multiples of 8
+ *   out      device bf16 [T][out_stride] (written)
+ *   ids, weights  device [T][k] (written)
+ *   ws       device, ep_few_tokens_workspace_bytes(T, k, inter) bytes, 16-byte
+ *            aligned; no state between calls, calls in flight at once need their own
+ */
+#define EP_MAX_FEW_TOKENS 64
+typedef struct ep_experts {
+    int32_t hidden, inter;
+    int32_t dtype; /* EP_DTYPE_BF16 or EP_DTYPE_FP8 */
+    ep_matrix_t gate, up, down;
+} ep_experts_t;
+size_t ep_few_tokens_workspace_bytes(int32_t num_tokens, int32_t top_k, int32_t inter);
+int ep_moe_few_tokens(const void *x, int64_t x_stride, int32_t num_tokens, const void *logits, int64_t logits_stride,
+                      const ep_gate_t *gate, const ep_experts_t *experts, void *out, int64_t out_stride, int32_t *ids,
+                      float *weights, void *ws, size_t ws_bytes, ep_stream_t stream);
+
+/*
+ * AdamW over many tensors in one launch (one for every 48 tensors), in place:
+ *   g = grad * grad_scale,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr wd) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32, each operation rounded.  state_bits 32: exp_avg, exp_avg_sq are
+ * float [numel].  state_bits 8: they are bytes [numel] with a scale byte c
+ * (2^(c - 127)) for each 128 elements in exp_avg_scale, exp_avg_sq_scale
+ * [ceil(numel / 128)]; m as sign, 4 bits of exponent, 3 of mantissa, v as 5 bits
+ * of exponent, 3 of mantissa (never 0 for v > 0), rounded stochastically from a
+ * hash of (seed, step, index of the tensor, element), so that a run repeats bit
+ * for bit.  Fresh states are all 0 with scale bytes 1.
+ * The array of descriptors is host memory and read at enqueue time.
+ */
+typedef struct ep_adamw_tensor {
+    float *param;
+    const void *grad;           /* fp32 or bf16, grad_dtype */
+    void *exp_avg, *exp_avg_sq;
+    uint8_t *exp_avg_scale, *exp_avg_sq_scale;
+    void *copy;                 /* bf16 [numel] of the new parameters, or NULL */
+    int64_t numel;              /* 0: skipped */
+} ep_adamw_tensor_t;
+typedef struct ep_adamw {
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    int64_t step;               /* from 1 */
+    uint32_t seed;
+    int32_t state_bits, grad_dtype;
+} ep_adamw_t;
+int ep_adamw_step(const ep_adamw_tensor_t *tensors, int32_t num_tensors, const ep_adamw_t *hp, ep_stream_t stream);
+
+/* The fp32 values of 8-bit states: exp_avg[i], exp_avg_sq[i] device float
+ * [numel] of tensor i (host arrays of pointers). */
+int ep_adamw_values(const ep_adamw_tensor_t *tensors, int32_t num_tensors, float *const *exp_avg,
+                    float *const *exp_avg_sq, ep_stream_t stream);
 
 /* Human-readable name of a return code. */
 const char *ep_status_string(int code);

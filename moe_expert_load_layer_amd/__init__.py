@@ -85,6 +85,8 @@ def lib() -> ctypes.CDLL:
                   "ep_slot_fill", "ep_balance_stats", "ep_dispatch_layout", "ep_replica_grad_reduce",
                   "ep_route_noalloc", "ep_route_pipelined"):
             getattr(L, f).restype = ctypes.c_int
+        from . import layer
+        layer.declare(L)
         _lib = L
     return _lib
 
@@ -468,3 +470,9 @@ def run_path(topk_ids: torch.Tensor, layout: Layout, stream=None):
     stats, imb, rank_load = ep_balance_stats(load, plan.phy_quota, layout, stream=stream)
     return dict(load=load, ws=ws, status=status, plan=plan, phys=phys, stats=stats, imbalance=imb,
                 rank_load=rank_load)
+
+
+from .layer import (  # noqa: E402,F401  (the operators around the balancer)
+    EP_DTYPE_BF16, EP_DTYPE_F32, EP_DTYPE_FP8, EP_MAX_FEW_TOKENS, AdamW, ep_few_tokens_workspace_bytes,
+    ep_gate_topk, ep_gate_topk_backward, ep_grouped_matmul, ep_grouped_wgrad, ep_moe_combine, ep_moe_few_tokens,
+    ep_quant_blocks, ep_quant_rows, ep_scale_stride, ep_swiglu_quant)

@@ -21,6 +21,16 @@ inline hipStream_t as_stream(ep_stream_t s) { return reinterpret_cast<hipStream_
 inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 inline int hip_rc(hipError_t e) { return e == hipSuccess ? EP_OK : EP_ERR_HIP; }
 
+bool pairs_ok(const int32_t *ids, int64_t N, int32_t P) {
+    if (N < 0 || N > kMaxPairs || P < 1 || P > kMaxPlans) return false;
+    if (N > 0 && (!ids || !aligned(ids, 4))) return false;
+    return true;
+}
+
+}  // namespace
+
+namespace ep {
+
 bool layout_ok(const ep_layout_t *L) {
     if (!L || !L->tables) return false;
     if (L->num_experts < 1 || L->num_experts > EP_MAX_EXPERTS) return false;
@@ -33,16 +43,6 @@ bool layout_ok(const ep_layout_t *L) {
     if (L->ranks_per_domain < 0) return false;
     return aligned(L->tables, 4);
 }
-
-bool pairs_ok(const int32_t *ids, int64_t N, int32_t P) {
-    if (N < 0 || N > kMaxPairs || P < 1 || P > kMaxPlans) return false;
-    if (N > 0 && (!ids || !aligned(ids, 4))) return false;
-    return true;
-}
-
-}  // namespace
-
-namespace ep {
 
 int check_histogram(const int32_t *topk_ids, int64_t N, int32_t P, const ep_layout_t *layout,
                     const int32_t *load, const void *ws, size_t ws_size, const uint32_t *status) {

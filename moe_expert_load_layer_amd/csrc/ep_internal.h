@@ -326,6 +326,7 @@ int resident_blocks(const void *fn, int threads, size_t lds);
 // Host-side argument checks of ep_load_histogram, ep_plan_quota and
 // ep_reroute (EP_OK or the error code the call returns); the no-allocation
 // chain runs all three before it enqueues anything.
+bool layout_ok(const ep_layout_t *L);
 int check_histogram(const int32_t *topk_ids, int64_t N, int32_t P, const ep_layout_t *layout,
                     const int32_t *load, const void *ws, size_t ws_size, const uint32_t *status);
 int check_plan(const int32_t *load, int32_t P, const ep_layout_t *layout, const int32_t *phy2log,

@@ -1,0 +1,139 @@
+// The gate: top-k expert IDs and weights from router logits, and its gradient.
+//
+// 16 lanes take a token (gate.h), a wave four, a workgroup 16.  Forward reads
+// the logits once and is bound by the k selection rounds; backward writes the
+// dense gradient rows, assembled in LDS, and is bound by HBM.
+#include "gate.h"
+
+namespace ep {
+
+bool gate_ok(const ep_gate_t *g) {
+    if (!g || g->num_experts < 1 || g->num_experts > kGateMaxExperts || !float_dtype(g->logits_dtype)) return false;
+    if (g->num_groups < 1 || g->num_groups > kGateMaxGroups || g->num_experts % g->num_groups != 0) return false;
+    if (g->topk_groups < 1 || g->topk_groups > g->num_groups) return false;
+    if (g->top_k < 1 || g->top_k > kGateMaxK || g->top_k > g->num_experts) return false;
+    return is_aligned(g->bias, 4) && g->scale - g->scale == 0;  // finite
+}
+
+GateArgs gate_args(const void *logits, int64_t stride, const ep_gate_t *g) {
+    GateArgs A;
+    const int width = g->logits_dtype == EP_DTYPE_BF16 ? 2 : 4;
+    A.logits = logits;
+    A.stride = stride;
+    A.bias = g->bias;
+    A.E = g->num_experts;
+    A.k = g->top_k;
+    A.G = g->topk_groups == g->num_groups ? 1 : g->num_groups;  // all groups stay: no limit
+    A.TG = g->topk_groups;
+    A.scale = g->scale;
+    A.bf16 = g->logits_dtype == EP_DTYPE_BF16;
+    A.vec = is_aligned(logits, 16) && (stride * width) % 16 == 0;
+    return A;
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokens = kThreads / kGateLanes;  // tokens of a workgroup
+
+template <int V>
+__global__ __launch_bounds__(kThreads) void gate_kernel(const GateArgs A, int64_t T, int32_t *__restrict__ ids,
+                                                        float *__restrict__ weights) {
+    __shared__ GateSlot slots[kTokens];
+    const int s = threadIdx.x / kGateLanes, lane = threadIdx.x % kGateLanes;
+    const int64_t t = (int64_t)blockIdx.x * kTokens + s;
+    int id;
+    float w;
+    gate_token<V>(A, t < T ? t : T - 1, &slots[s], id, w);  // rows past the end repeat the last token
+    if (t < T && lane < A.k) {
+        ids[t * A.k + lane] = id;
+        weights[t * A.k + lane] = w;
+    }
+}
+
+// dl_j = w_j (g_j - sum_i w_i g_i / scale) at the chosen experts, 0 elsewhere
+template <bool kBf16>
+__global__ __launch_bounds__(kThreads) void gate_backward_kernel(const int32_t *__restrict__ ids,
+                                                                 const float *__restrict__ weights,
+                                                                 const float *__restrict__ grad, int64_t T, int E,
+                                                                 int k, float inv_scale, void *__restrict__ out) {
+    extern __shared__ float lds[];  // [kTokens][E]
+    const int s = threadIdx.x / kGateLanes, lane = threadIdx.x % kGateLanes;
+    const int64_t t0 = (int64_t)blockIdx.x * kTokens, t = t0 + s;
+    for (int i = threadIdx.x; i < kTokens * E; i += kThreads) lds[i] = 0.0f;
+    __syncthreads();
+    const bool on = t < T && lane < k;
+    const int id = on ? ids[t * k + lane] : -1;
+    const bool use = id >= 0 && id < E;
+    const float w = use ? weights[t * k + lane] : 0.0f;
+    const float g = use ? grad[t * k + lane] : 0.0f;
+    const float mean = row_sum_f32(w * g) * inv_scale;
+    if (use) lds[s * E + id] = w * (g - mean);
+    __syncthreads();
+    const int64_t n = min((int64_t)kTokens, T - t0) * E, o = t0 * E;
+    // the workgroup's rows are one run of memory; 16-byte stores, the end in single ones
+    constexpr int kPer = kBf16 ? 8 : 4;
+    const int64_t whole = (o % kPer == 0 && ((uintptr_t)out & 15) == 0) ? n / kPer : 0;
+    for (int64_t i = threadIdx.x; i < whole; i += kThreads) {
+        const float *p = lds + i * kPer;
+        if constexpr (kBf16) {
+            const u32x4 w4{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])};
+            reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(out) + o)[i] = w4;
+        } else {
+            reinterpret_cast<f32x4 *>(static_cast<float *>(out) + o)[i] = f32x4{p[0], p[1], p[2], p[3]};
+        }
+    }
+    for (int64_t i = whole * kPer + threadIdx.x; i < n; i += kThreads) {
+        if constexpr (kBf16)
+            static_cast<uint16_t *>(out)[o + i] = to_bf16(lds[i]);
+        else
+            static_cast<float *>(out)[o + i] = lds[i];
+    }
+}
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_gate_topk(const void *logits, int64_t stride, int64_t num_tokens, const ep_gate_t *gate,
+                            int32_t *ids, float *weights, ep_stream_t stream) {
+    if (!gate_ok(gate) || num_tokens < 0 || num_tokens > kMaxBlocks * kTokens || stride < gate->num_experts)
+        return EP_ERR_INVALID_ARG;
+    if (num_tokens == 0) return EP_OK;
+    const size_t width = gate->logits_dtype == EP_DTYPE_BF16 ? 2 : 4;
+    if (!logits || !ids || !weights || !is_aligned(logits, width) || !is_aligned(ids, 4) || !is_aligned(weights, 4))
+        return EP_ERR_INVALID_ARG;
+    const GateArgs A = gate_args(logits, stride, gate);
+    const dim3 grid((uint32_t)ceil_div(num_tokens, kTokens));
+    const hipStream_t s = to_stream(stream);
+    const int per = (A.E + kGateLanes - 1) / kGateLanes;
+    if (per <= 8) gate_kernel<8><<<grid, kThreads, 0, s>>>(A, num_tokens, ids, weights);
+    else if (per <= 16) gate_kernel<16><<<grid, kThreads, 0, s>>>(A, num_tokens, ids, weights);
+    else if (per <= 24) gate_kernel<24><<<grid, kThreads, 0, s>>>(A, num_tokens, ids, weights);
+    else if (per <= 32) gate_kernel<32><<<grid, kThreads, 0, s>>>(A, num_tokens, ids, weights);
+    else gate_kernel<64><<<grid, kThreads, 0, s>>>(A, num_tokens, ids, weights);
+    return rc_of(hipGetLastError());
+}
+
+extern "C" int ep_gate_topk_backward(const int32_t *ids, const float *weights, const float *grad_weights,
+                                     int64_t num_tokens, const ep_gate_t *gate, void *grad_logits,
+                                     ep_stream_t stream) {
+    if (!gate_ok(gate) || num_tokens < 0 || num_tokens > kMaxBlocks * kTokens) return EP_ERR_INVALID_ARG;
+    if (num_tokens == 0) return EP_OK;
+    const bool bf16 = gate->logits_dtype == EP_DTYPE_BF16;
+    if (!ids || !weights || !grad_weights || !grad_logits || !is_aligned(ids, 4) || !is_aligned(weights, 4) ||
+        !is_aligned(grad_weights, 4) || !is_aligned(grad_logits, bf16 ? 2 : 4))
+        return EP_ERR_INVALID_ARG;
+    const float inv = gate->scale != 0.0f ? 1.0f / gate->scale : 0.0f;
+    const dim3 grid((uint32_t)ceil_div(num_tokens, kTokens));
+    const size_t lds = (size_t)kTokens * gate->num_experts * sizeof(float);
+    const hipStream_t s = to_stream(stream);
+    if (bf16)
+        gate_backward_kernel<true><<<grid, kThreads, lds, s>>>(ids, weights, grad_weights, num_tokens,
+                                                               gate->num_experts, gate->top_k, inv, grad_logits);
+    else
+        gate_backward_kernel<false><<<grid, kThreads, lds, s>>>(ids, weights, grad_weights, num_tokens,
+                                                                gate->num_experts, gate->top_k, inv, grad_logits);
+    return rc_of(hipGetLastError());
+}
