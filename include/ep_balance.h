@@ -539,7 +539,7 @@ int ep_moe_combine(const void *y, int64_t rows, const int32_t *pos, const float 
  *            bytes past a row's columns must be 0); hidden and inter multiples of 8
  *   out      device bf16 [T][out_stride] (written)
  *   ids, weights  device [T][k] (written)
- *   ws       device, ep_few_tokens_workspace_bytes(T, k, inter) bytes, 16-byte
+ *   ws       device, ep_few_tokens_workspace_bytes(T, k, hidden, inter) bytes, 16-byte
  *            aligned; no state between calls, calls in flight at once need their own
  */
 #define EP_MAX_FEW_TOKENS 64
@@ -548,7 +548,7 @@ typedef struct ep_experts {
     int32_t dtype; /* EP_DTYPE_BF16 or EP_DTYPE_FP8 */
     ep_matrix_t gate, up, down;
 } ep_experts_t;
-size_t ep_few_tokens_workspace_bytes(int32_t num_tokens, int32_t top_k, int32_t inter);
+size_t ep_few_tokens_workspace_bytes(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t inter);
 int ep_moe_few_tokens(const void *x, int64_t x_stride, int32_t num_tokens, const void *logits, int64_t logits_stride,
                       const ep_gate_t *gate, const ep_experts_t *experts, void *out, int64_t out_stride, int32_t *ids,
                       float *weights, void *ws, size_t ws_bytes, ep_stream_t stream);

@@ -3,36 +3,48 @@
 //   down  out_t = sum_j w_tj Wd_e h_p
 //
 // Bound: HBM.  Every distinct expert's three matrices are read once, which is
-// all but a fraction of a percent of the bytes.  The tokens of one expert are
-// the 16 columns of a matrix instruction (2 or 4 column tiles for experts
-// with more), the weights its 16 rows, loaded straight into registers: no
-// weight is used twice by a workgroup, so LDS would only add a hop.
+// all but a fraction of a percent of the bytes.  (An expert with more than 32
+// tokens is read once for every 32.)
 //
-// up: one work item is 8 rows of the gate and the same 8 rows of the up matrix
-// (one 16-row tile) of one expert; its 8 waves take every eighth 128-byte
-// window of the rows and meet in LDS, in wave order.  A fixed grid of two
-// workgroups per CU walks the items, so that each workgroup chooses experts and
-// groups pairs once.  h is kept as the sum of two bf16 (16 bits of mantissa):
-// one bf16 would add as much error as the output's own rounding.
-// down: one workgroup owns 16 rows of the output over all experts, its waves
-// equal shares of the (expert, window) sequence; partial sums stay per wave in
-// LDS and are added in wave order.  No atomics on sums: results do not depend
-// on scheduling.
+// Both kernels stream: a workgroup takes 64 weight rows of an expert and walks
+// them in windows of 128 bytes a row, together with the same window of the
+// expert's columns (tokens, or pairs' h).  Windows go from memory into a ring of
+// LDS stages without passing registers; all but one stage of the ring are in
+// flight, across the borders between experts too, and one barrier a window
+// hands a stage over.  Each of the 4 waves multiplies its own 16 rows, so no
+// sum crosses waves, and a column is fetched once for 64 rows.
+//
+// up: 64 rows are 32 of gate and the same 32 of up, 8 and 8 in each wave, whose
+// halves exchange them for silu.  h is kept as the sum of two bf16 (16 bits of
+// mantissa): one bf16 would add as much error as the output's own rounding.
+// down: the high and low parts of 8 pairs' h are the 16 columns of one matrix
+// instruction.  The (expert, window) sequence of 64 output rows is cut into
+// shares so that about 512 workgroups run; the last share to arrive adds all of
+// them in order.  No atomics on sums: results do not depend on scheduling.
 //
 // 8-bit weights: a window is 128 values with one scale byte; v_cvt_scalef32
 // gives bf16 exactly (3 bits of mantissa, power-of-two scale), so products and
 // sums are those of the bf16 path.
 #include "gate.h"
+#include "groups.h"
 
 namespace ep {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kMaxTokens = EP_MAX_FEW_TOKENS;
 constexpr int kMaxPairs = kMaxTokens * kGateMaxK;
-constexpr int kUnroll = 4;         // windows whose loads are in flight together
-constexpr int kWindowBytes = 128;  // of one weight row
+constexpr int kMaxWidth = 65536;  // hidden and inter
+constexpr int kRows = kWaves * 16;     // weight rows of a workgroup
+constexpr int kUpRows = kRows / 2;     // of gate and of up
+constexpr int kWindowBytes = 128;      // of one row
+constexpr int kScaleUnits = 512;       // windows whose scale bytes are in LDS at a time
+// pairs of one expert that are multiplied together: 8 where no expert can have more
+constexpr int kFew = 8, kUpMany = 32, kDownMany = 16;
+constexpr int kMaxEntries = kGateMaxExperts + kMaxPairs / kDownMany;
+
+__device__ __align__(16) const uint32_t kNothing[4] = {0, 0, 0, 0};
 
 struct Matrix {
     const uint8_t *data;
@@ -50,132 +62,68 @@ struct FewArgs {
     float *weights;
     uint16_t *out;
     uint16_t *hhi, *hlo;  // [T * k][I]
+    int32_t *arrivals;    // of each block of output rows, zeroed by the first kernel
+    float *sums;          // [shares][T][H]
 };
 
-// The pairs of each chosen expert, in LDS.
+// The pairs of each chosen expert, in LDS.  An entry is an expert with up to
+// kCols of its pairs.
 struct Lists {
-    int32_t ids[kMaxPairs];
-    uint16_t pair[kMaxPairs];             // pairs ordered by expert
-    uint16_t expert[kGateMaxExperts];     // the chosen experts, ascending
-    uint16_t start[kGateMaxExperts + 1];  // their first entry in `pair`
-    int32_t count[kGateMaxExperts];       // pairs of each expert, then fill cursors
-    int32_t active;
+    uint16_t pair[kMaxPairs];     // pairs ordered by expert
+    uint16_t expert[kMaxEntries];
+    uint16_t start[kMaxEntries];  // the entry's first place in `pair`
+    uint8_t count[kMaxEntries];
+    int32_t entries;
 };
 
-// L->ids holds T * k IDs.  The order of an expert's pairs does not matter to
-// any result: a pair is a column of its own.
-__device__ void build_lists(Lists *L, int pairs, int E) {
-    for (int e = threadIdx.x; e < E; e += kThreads) L->count[e] = 0;
+// What the lists are made from; it lies where the ring's stages come later.
+struct Scratch {
+    int32_t ids[kMaxPairs];
+    uint32_t tokens[2][kGateMaxExperts];  // of each expert, a bit each
+    uint16_t first[kGateMaxExperts];      // of each expert in `pair`
+    GateSlot slot[kThreads / kGateLanes];
+};
+
+// W->ids holds T * k IDs, every expert at most once for a token.  The pairs of
+// an expert are ordered by token, in every workgroup alike: its entries are
+// worked on by different ones.
+template <int kCols>
+__device__ void build_lists(Lists *L, Scratch *W, int T, int k, int E) {
+    static_assert(kMaxTokens == 64, "a bit for each token");
+    for (int e = threadIdx.x; e < E; e += kThreads) W->tokens[0][e] = W->tokens[1][e] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += kThreads)
-        if (L->ids[p] >= 0) atomicAdd(&L->count[L->ids[p]], 1);
+    for (int p = threadIdx.x; p < T * k; p += kThreads) {
+        const int t = p / k;
+        if (W->ids[p] >= 0) atomicOr(&W->tokens[t / 32][W->ids[p]], 1u << (t % 32));
+    }
     __syncthreads();
     if (threadIdx.x < kWave) {
-        int act = 0, first = 0;
+        int entries = 0, first = 0;
         for (int e0 = 0; e0 < E; e0 += kWave) {
             const int e = e0 + (int)threadIdx.x;
-            const int c = e < E ? L->count[e] : 0;
-            const uint64_t on = __ballot(c > 0);
-            const int incl = wave_incl_scan_i32(c);
-            if (c > 0) {
-                const int a = act + __popcll(on & lanemask_lt());
+            const int c = e < E ? __popc(W->tokens[0][e]) + __popc(W->tokens[1][e]) : 0;
+            const int n = (c + kCols - 1) / kCols;
+            const int places = wave_incl_scan_i32(c), slots = wave_incl_scan_i32(n);
+            for (int i = 0; i < n; i++) {
+                const int a = entries + slots - n + i;
                 L->expert[a] = (uint16_t)e;
-                L->start[a] = (uint16_t)(first + incl - c);
+                L->start[a] = (uint16_t)(first + places - c + i * kCols);
+                L->count[a] = (uint8_t)min(kCols, c - i * kCols);
             }
-            if (e < E) L->count[e] = first + incl - c;
-            act += __popcll(on);
-            first += __builtin_amdgcn_readlane(incl, kWave - 1);
+            if (e < E) W->first[e] = (uint16_t)(first + places - c);
+            entries += __builtin_amdgcn_readlane(slots, kWave - 1);
+            first += __builtin_amdgcn_readlane(places, kWave - 1);
         }
-        if (threadIdx.x == 0) {
-            L->active = act;
-            L->start[act] = (uint16_t)first;
-        }
+        if (threadIdx.x == 0) L->entries = entries;
     }
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += kThreads)
-        if (L->ids[p] >= 0) L->pair[atomicAdd(&L->count[L->ids[p]], 1)] = (uint16_t)p;
+    for (int p = threadIdx.x; p < T * k; p += kThreads) {
+        const int e = W->ids[p], t = p / k;
+        if (e < 0) continue;
+        const uint64_t all = ((uint64_t)W->tokens[1][e] << 32) | W->tokens[0][e];
+        L->pair[W->first[e] + __popcll(all & ((1ull << t) - 1))] = (uint16_t)p;
+    }
     __syncthreads();
-}
-
-// The 128-byte window `win` of a weight row, as this lane's part: bf16 two
-// times 8 values at k = 64 win + 8 q and + 32, 8 bits two times 16 values at
-// k = 128 win + 32 q and + 16.
-template <bool kFp8>
-__device__ __forceinline__ void load_window(const uint8_t *row, int win, int q, int K, u32x4 (&w)[2]) {
-#pragma unroll
-    for (int j = 0; j < 2; j++) {
-        int off = win * kWindowBytes + (kFp8 ? q * 32 + j * 16 : q * 16 + j * 64);
-        if (!kFp8 && off >= K * 2) off = 0;  // past the row's end: not used (8-bit rows are whole windows)
-        w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(row + off));
-    }
-}
-
-template <bool kFp8>
-constexpr int kSteps = kFp8 ? 4 : 2;  // matrix instructions of a window
-
-// first value of step s of window win in this lane
-template <bool kFp8>
-__device__ __forceinline__ int step_k(int win, int q, int s) {
-    return kFp8 ? win * 128 + q * 32 + s * 8 : win * 64 + q * 8 + s * 32;
-}
-
-// the weights of step s as 8 bf16
-template <bool kFp8>
-__device__ __forceinline__ bf16x8 step_weights(const u32x4 (&w)[2], int s, float scale) {
-    if constexpr (kFp8) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        union {
-            bf16x2 h[4];
-            bf16x8 v;
-        } u;
-        const uint32_t a = w[s / 2][2 * (s % 2)], b = w[s / 2][2 * (s % 2) + 1];
-        u.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false);
-        u.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true);
-        u.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false);
-        u.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true);
-        return u.v;
-    } else {
-        return __builtin_bit_cast(bf16x8, w[s]);
-    }
-}
-
-// acc[n] += rows x columns over the windows first, first + stride, ... below
-// last.  col[n][c]: this lane's column of tile n, kParts arrays summed.
-template <bool kFp8, int NT, int kParts>
-__device__ __forceinline__ void stream_rows(const uint8_t *row, const uint8_t *scale, int K, int first, int last,
-                                            int stride, int q, const uint16_t *const (&col)[kParts][NT],
-                                            f32x4 (&acc)[NT]) {
-    for (int w0 = first; w0 < last; w0 += kUnroll * stride) {
-        u32x4 w[kUnroll][2];
-        float sc[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; u++) {
-            const int win = min(w0 + u * stride, last - 1);  // past the end: loaded, not used
-            load_window<kFp8>(row, win, q, K, w[u]);
-            sc[u] = kFp8 ? pow2_of(scale[win]) : 1.0f;
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; u++) {
-            const int win = w0 + u * stride;
-            if (win >= last) break;
-#pragma unroll
-            for (int s = 0; s < kSteps<kFp8>; s++) {
-                const int k = step_k<kFp8>(win, q, s);
-                const bool in = k < K;  // K is a multiple of 8
-                const u32x4 zero{0, 0, 0, 0};
-                bf16x8 a = step_weights<kFp8>(w[u], s, sc[u]);
-                if (!in) a = __builtin_bit_cast(bf16x8, zero);
-#pragma unroll
-                for (int c = 0; c < kParts; c++)
-#pragma unroll
-                    for (int n = 0; n < NT; n++) {
-                        const u32x4 b = in ? *reinterpret_cast<const u32x4 *>(col[c][n] + k) : zero;
-                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, b), acc[n], 0,
-                                                                         0, 0);
-                    }
-            }
-        }
-    }
 }
 
 template <bool kFp8>
@@ -188,168 +136,447 @@ __device__ __forceinline__ int64_t row_bytes(int K) {
     return kFp8 ? (int64_t)((K + 127) / 128) * 128 : (int64_t)K * 2;
 }
 
-// One item: rows i0 .. i0 + 7 of gate and up of one expert, columns = its pairs.
-template <bool kFp8, int NT>
-__device__ __forceinline__ void up_item(const FewArgs &A, const Lists *L, int a, int i0, float *red) {
-    const int wave = threadIdx.x / kWave, l = lane_id(), r = l & 15, q = l >> 4;
-    const int e = L->expert[a], first = L->start[a], n = L->start[a + 1] - first;
-    const int i = min(i0 + (r & 7), A.I - 1);
-    const Matrix &M = r < 8 ? A.wg : A.wu;
-    const uint8_t *row = M.data + e * M.stride + i * row_bytes<kFp8>(A.H);
-    const int nw = windows_of<kFp8>(A.H);
-    const uint8_t *scale = kFp8 ? M.scale + e * M.scale_stride + (int64_t)(i / kScaleBlock) * nw : nullptr;
-    const uint16_t *col[1][NT];
-    f32x4 acc[NT];
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-        const int c = min(t * 16 + r, n - 1);  // columns past the end repeat the last
-        col[0][t] = A.x + (int64_t)(L->pair[first + c] / A.k) * A.x_stride;
-        acc[t] = f32x4{0, 0, 0, 0};
+// Waits until at most n of this wave's loads are in flight; n is the same in
+// every lane.  The instruction's count is a constant, hence the cases.
+__device__ __forceinline__ void wait_loads_but(int n) {
+    switch (n) {
+#define EP_WAIT(N) \
+    case N: asm volatile("s_waitcnt vmcnt(" #N ")" ::: "memory"); break;
+        EP_WAIT(2) EP_WAIT(3) EP_WAIT(4) EP_WAIT(5) EP_WAIT(6)
+#undef EP_WAIT
+        default: wait_loads();
     }
-    stream_rows<kFp8, NT, 1>(row, scale, A.H, wave, nw, kWaves, q, col, acc);
-    // red [wave][column][16 rows]: a lane's 4 rows are one 16-byte store
-#pragma unroll
-    for (int t = 0; t < NT; t++)
-        *reinterpret_cast<f32x4 *>(red + ((wave * NT + t) * 16 + r) * 16 + 4 * q) = acc[t];
-    __syncthreads();
-    for (int o = threadIdx.x; o < NT * 16 * 8; o += kThreads) {
-        const int c = o / 8, j = o % 8;
-        if (c >= n || i0 + j >= A.I) continue;
-        float g = 0.0f, u = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; w++) {
-            g += red[(w * NT * 16 + c) * 16 + j];
-            u += red[(w * NT * 16 + c) * 16 + 8 + j];
-        }
-        const float h = g / (1.0f + expf(-g)) * u;
-        const int64_t at = (int64_t)L->pair[first + c] * A.I + i0 + j;
-        const uint16_t hi = to_bf16(h);
-        const float rest = h - __builtin_bit_cast(float, (uint32_t)hi << 16);
-        A.hhi[at] = hi;
-        // an h that is infinite as bf16, or NaN, has no rest
-        A.hlo[at] = to_bf16(fabsf(rest) < INFINITY ? rest : 0.0f);
-    }
-    __syncthreads();
 }
 
-template <bool kFp8, int V>
-__global__ __launch_bounds__(kThreads, 4) void up_kernel(const FewArgs A) {
+// The ring of one workgroup.  kParts: arrays of column values (x, or h's high
+// and low parts).  A column's window is kHalves rows of 128 bytes.  LDS rows are
+// 128 bytes, their 16-byte chunks exchanged by the row's low 3 bits.
+template <bool kFp8, int kCols, int kParts>
+struct Ring {
+    static constexpr int kHalves = kFp8 ? 2 : 1;
+    static constexpr int kColRows = kCols * kParts * kHalves;  // row of column c, part p, half h: (p * kHalves + h) * kCols + c
+    static constexpr int kColLoads = kColRows / 8;             // loads of 1 KiB
+    static constexpr int kMine = (kColLoads + kWaves - 1) / kWaves;
+    static constexpr int kStage = (kRows + kColRows) * 128;
+    static constexpr int kStages = 3;  // more would leave room for fewer workgroups: slower in every case measured
+    static constexpr int kTiles = kParts == 2 ? kCols / 8 : (kCols + 15) / 16;
+
+    uint8_t *lds;
+    int wave, K;
+    const uint8_t *w[2];  // this lane's source of the wave's loads, at window 0
+    const uint8_t *col[kMine];
+    int n;                     // columns of the windows being fetched
+    int flying;  // loads of the newest window
+
+    __device__ __forceinline__ static int chunk() { return (lane_id() & 7) ^ (lane_id() >> 3); }
+    // row of the weights that load i fetches for this lane, and its row of columns
+    __device__ __forceinline__ int weight_row(int i) const { return (wave + i * kWaves) * 8 + lane_id() / 8; }
+    __device__ __forceinline__ int column_row(int i) const { return (wave + i * kWaves) * 8 + lane_id() / 8; }
+
+    // Only the groups of 8 columns that the entry has are fetched.
+    __device__ __forceinline__ void issue(int slot, int win, bool partial) {
+        uint8_t *s = lds + slot * kStage;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint8_t *p = w[i] + win * kWindowBytes;
+            if (!kFp8 && partial && win * 64 + chunk() * 8 >= K) p = reinterpret_cast<const uint8_t *>(kNothing);
+            load_lds_1k(p, s + (wave + i * kWaves) * 1024);
+        }
+        int count = 2;
+#pragma unroll
+        for (int i = 0; i < kMine; i++) {
+            const int load = wave + i * kWaves;
+            if (load >= kColLoads || load % (kCols / 8) * 8 >= n) continue;
+            const uint8_t *p = col[i] + win * kWindowBytes * kHalves;
+            const int h = load / (kCols / 8) % kHalves;
+            if (partial && (win * kHalves + h) * 64 + chunk() * 8 >= K) p = reinterpret_cast<const uint8_t *>(kNothing);
+            load_lds_1k(p, s + kRows * 128 + load * 1024);
+            count++;
+        }
+        flying = count;
+    }
+
+    // waits until all but the newest window's loads are there
+    __device__ __forceinline__ void arrive() const {
+        static_assert(kStages == 3 && 2 + kMine <= 6, "one window stays in flight, its loads have a case");
+        wait_loads_but(flying);
+        __syncthreads();
+    }
+
+    // acc[t] += this wave's 16 rows x the columns of tile t, for n columns
+    __device__ __forceinline__ void multiply(int slot, int n, float scale, f32x4 (&acc)[kTiles]) const {
+        const uint8_t *tw = lds + slot * kStage + wave * 16 * 128, *tc = lds + slot * kStage + kRows * 128;
+        const int l = lane_id(), r = l & 15, q = l >> 4;
+        auto at = [](const uint8_t *t, int row, int c) {
+            return *reinterpret_cast<const u32x4 *>(t + row * 128 + ((c ^ (row & 7)) << 4));
+        };
+        constexpr int kPer = kParts == 2 ? 8 : 16;  // pairs of a tile
+        auto column = [&](int t, int h, int c) {
+            const int pair = kParts == 2 ? t * 8 + (r & 7) : (t * 16 + r) % kCols;
+            const int part = kParts == 2 ? r >> 3 : 0;
+            return __builtin_bit_cast(bf16x8, at(tc, (part * kHalves + h) * kCols + pair, c));
+        };
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const u32x4 raw = at(tw, r, q + 4 * h);
+            if constexpr (kFp8) {
+                // 16 values at k = 16 (q + 4 h), as two steps of 8
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+                    union {
+                        bf16x2 h2[4];
+                        bf16x8 v;
+                    } a;
+                    a.h2[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * j], scale, false);
+                    a.h2[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * j], scale, true);
+                    a.h2[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * j + 1], scale, false);
+                    a.h2[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * j + 1], scale, true);
+#pragma unroll
+                    for (int t = 0; t < kTiles; t++)
+                        if (t * kPer < n)
+                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, column(t, h, 2 * q + j), acc[t], 0, 0, 0);
+                }
+            } else {
+                // 8 values at k = 8 (q + 4 h)
+                const bf16x8 a = __builtin_bit_cast(bf16x8, raw);
+#pragma unroll
+                for (int t = 0; t < kTiles; t++)
+                    if (t * kPer < n)
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, column(t, 0, q + 4 * h), acc[t], 0, 0, 0);
+            }
+        }
+    }
+};
+
+template <bool kFp8, int kCols, int V>
+__global__ __launch_bounds__(kThreads) void up_kernel(const FewArgs A) {
+    typedef Ring<kFp8, kCols, 1> R;
+    __shared__ __align__(16) uint8_t stages[R::kStages * R::kStage];
     __shared__ Lists L;
-    __shared__ union {
-        GateSlot slot[kThreads / kGateLanes];
-        float red[kWaves * 4 * 256];
-    } S;
+    __shared__ uint8_t scales[kFp8 ? 2 * kScaleUnits : 2];
+    static_assert(sizeof(Scratch) <= sizeof(stages), "the scratch fits the stages");
+    Scratch *W = reinterpret_cast<Scratch *>(stages);
     // every workgroup chooses for itself; the first one writes the choice
     constexpr int kPass = kThreads / kGateLanes;
     for (int t0 = 0; t0 < A.T; t0 += kPass) {
         const int s = threadIdx.x / kGateLanes, j = threadIdx.x % kGateLanes, t = t0 + s;
         int id;
         float w;
-        gate_token<V>(A.gate, min(t, A.T - 1), &S.slot[s], id, w);
+        gate_token<V>(A.gate, min(t, A.T - 1), &W->slot[s], id, w);
         if (t < A.T && j < A.k) {
-            L.ids[t * A.k + j] = id;
+            W->ids[t * A.k + j] = id;
             if (blockIdx.x == 0) {
                 A.ids[t * A.k + j] = id;
                 A.weights[t * A.k + j] = w;
             }
         }
     }
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < (A.H + kRows - 1) / kRows; i += kThreads) A.arrivals[i] = 0;
     __syncthreads();
-    build_lists(&L, A.T * A.k, A.gate.E);
-    const int tiles = (A.I + 7) / 8, items = L.active * tiles;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int a = it / tiles, i0 = (it - a * tiles) * 8;
-        const int n = L.start[a + 1] - L.start[a];
-        if (n <= 16) up_item<kFp8, 1>(A, &L, a, i0, S.red);
-        else if (n <= 32) up_item<kFp8, 2>(A, &L, a, i0, S.red);
-        else up_item<kFp8, 4>(A, &L, a, i0, S.red);
-    }
-}
+    build_lists<kCols>(&L, W, A.T, A.k, A.gate.E);
 
-// windows [w0, w1) of expert a for output rows o0 .. o0 + 15, into `part`
-template <bool kFp8, int NT>
-__device__ __forceinline__ void down_run(const FewArgs &A, const Lists *L, int a, int o0, int w0, int w1,
-                                         float *part) {
-    const int l = lane_id(), r = l & 15, q = l >> 4;
-    const int e = L->expert[a], first = L->start[a], n = L->start[a + 1] - first;
-    const int o = min(o0 + r, A.H - 1);
-    const uint8_t *row = A.wd.data + e * A.wd.stride + o * row_bytes<kFp8>(A.I);
-    const uint8_t *scale =
-        kFp8 ? A.wd.scale + e * A.wd.scale_stride + (int64_t)(o / kScaleBlock) * windows_of<kFp8>(A.I) : nullptr;
-    const uint16_t *col[2][NT];
-    f32x4 acc[NT];
+    // this workgroup's items (an entry's 32 rows of gate and of up), each nw windows
+    const int tiles = (A.I + kUpRows - 1) / kUpRows, items = L.entries * tiles, nw = windows_of<kFp8>(A.H);
+    if ((int)blockIdx.x >= items) return;
+    const int units = ((items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * nw;
+    const bool partial = A.H % (64 * R::kHalves) != 0;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = lane_id(), r = l & 15, q = l >> 4;
+    R ring;
+    ring.lds = stages;
+    ring.wave = wave;
+    ring.K = A.H;
+
+    int pu = 0, pit = blockIdx.x, pwin = 0;  // the next window to fetch
+    auto sources = [&] {
+        const int a = pit / tiles, i0 = (pit - a * tiles) * kUpRows, e = L.expert[a], first = L.start[a];
+        const int n = ring.n = __builtin_amdgcn_readfirstlane(L.count[a]);
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-        const int64_t at = (int64_t)L->pair[first + min(t * 16 + r, n - 1)] * A.I;
-        col[0][t] = A.hhi + at;
-        col[1][t] = A.hlo + at;
-        acc[t] = f32x4{0, 0, 0, 0};
-    }
-    stream_rows<kFp8, NT, 2>(row, scale, A.I, w0, w1, 1, q, col, acc);
-    // the wave's own sums: an expert has a token once, so lanes do not meet
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-        const int c = t * 16 + r;
-        if (c < n) {
-            const int p = L->pair[first + c];
-            f32x4 *d = reinterpret_cast<f32x4 *>(part + (p / A.k) * 16 + 4 * q);
-            const float w = A.weights[p];
-            f32x4 v = *d;
-#pragma unroll
-            for (int i = 0; i < 4; i++) v[i] += w * acc[t][i];
-            *d = v;
+        for (int i = 0; i < 2; i++) {
+            // rows 16 w .. + 7 are gate's 8 w .. + 7, the next 8 up's
+            const int row = ring.weight_row(i), o = min(i0 + row / 16 * 8 + row % 8, A.I - 1);
+            const uint8_t *m = row % 16 < 8 ? A.wg.data + e * A.wg.stride : A.wu.data + e * A.wu.stride;
+            ring.w[i] = m + o * row_bytes<kFp8>(A.H) + R::chunk() * 16;
         }
+#pragma unroll
+        for (int i = 0; i < R::kMine; i++) {
+            const int c = ring.column_row(i) % kCols, h = ring.column_row(i) / kCols;
+            const int t = L.pair[first + min(c, n - 1)] / A.k;  // columns past the end repeat the last
+            ring.col[i] = reinterpret_cast<const uint8_t *>(A.x + t * A.x_stride) + (h % R::kHalves) * 128 + R::chunk() * 16;
+        }
+    };
+    // past the last window that one is fetched again: the count of loads stays
+    auto produce = [&](int slot) {
+        ring.issue(slot, pwin, partial);
+        pu++;
+        if (pu < units && ++pwin == nw) {
+            pwin = 0;
+            pit += gridDim.x;
+            sources();
+        }
+    };
+    sources();
+#pragma unroll
+    for (int s = 0; s < R::kStages - 1; s++) produce(s);
+
+    f32x4 acc[R::kTiles];
+#pragma unroll
+    for (int t = 0; t < R::kTiles; t++) acc[t] = f32x4{0, 0, 0, 0};
+    int slot = 0, it = blockIdx.x, win = 0;
+    for (int u = 0; u < units; u++) {
+        if (kFp8 && u % kScaleUnits == 0) {
+            if (u > 0) __syncthreads();  // those before have been read
+            for (int i = threadIdx.x; i < 2 * min(kScaleUnits, units - u); i += kThreads) {
+                const int un = u + i / 2, b = blockIdx.x + un / nw * gridDim.x, a = b / tiles, e = L.expert[a];
+                const int block = (b - a * tiles) * kUpRows / kScaleBlock;
+                const uint8_t *m = i % 2 ? A.wu.scale + e * A.wu.scale_stride : A.wg.scale + e * A.wg.scale_stride;
+                scales[i] = m[(int64_t)block * nw + un % nw];
+            }
+        }
+        ring.arrive();
+        produce(slot == 0 ? R::kStages - 1 : slot - 1);
+        const int a = it / tiles, n = __builtin_amdgcn_readfirstlane(L.count[a]);
+        float scale = 1.0f;
+        if constexpr (kFp8) scale = pow2_of(scales[u % kScaleUnits * 2 + (r >> 3)]);
+        ring.multiply(slot, n, scale, acc);
+        slot = slot == R::kStages - 1 ? 0 : slot + 1;
+        if (++win < nw) continue;
+        // lanes 0 .. 31 have gate's 4 rows of a column, lanes 32 .. 63 up's
+        const int i0 = (it - a * tiles) * kUpRows + wave * 8 + (q & 1) * 4;
+#pragma unroll
+        for (int t = 0; t < R::kTiles; t++) {
+            if (t * 16 >= n) break;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float g = acc[t][i], up = __shfl_xor(acc[t][i], 32);
+                const float h = g / (1.0f + expf(-g)) * up;
+                hi[i] = to_bf16(h);
+                const float rest = h - __builtin_bit_cast(float, hi[i] << 16);
+                // an h that is infinite as bf16, or NaN, has no rest
+                lo[i] = to_bf16(fabsf(rest) < INFINITY ? rest : 0.0f);
+            }
+            const int c = t * 16 + r;
+            if (q < 2 && c < n && i0 < A.I) {  // I is a multiple of 8
+                const int64_t at = (int64_t)L.pair[L.start[a] + c] * A.I + i0;
+                *reinterpret_cast<u32x2 *>(A.hhi + at) = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
+                *reinterpret_cast<u32x2 *>(A.hlo + at) = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
+            }
+            acc[t] = f32x4{0, 0, 0, 0};
+        }
+        win = 0;
+        it += gridDim.x;
     }
+    wait_loads();  // those that nobody reads
 }
 
-template <bool kFp8>
-__global__ __launch_bounds__(kThreads, 4) void down_kernel(const FewArgs A) {
+// Shares of the weights that the workgroups of one block of output rows take:
+// about 512 workgroups in all, shares of 4 windows at least.
+int down_shares(int T, int k, int H, int I) {
+    const int64_t blocks = ceil_div(H, kRows), windows = (int64_t)T * k * ceil_div(I, 64);
+    const int64_t want = 512 / blocks < windows / 4 ? 512 / blocks : windows / 4;
+    return want < 1 ? 1 : want > 32 ? 32 : (int)want;
+}
+
+__device__ __forceinline__ void store_past_l2(uint64_t *p, float a, float b) {
+    const uint64_t v = __builtin_bit_cast(uint32_t, a) | (uint64_t)__builtin_bit_cast(uint32_t, b) << 32;
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <bool kFp8, int kCols>
+__global__ __launch_bounds__(kThreads) void down_kernel(const FewArgs A) {
+    typedef Ring<kFp8, kCols, 2> R;
+    __shared__ __align__(16) uint8_t stages[R::kStages * R::kStage];
     __shared__ Lists L;
+    __shared__ float weights[kMaxPairs];
+    __shared__ uint8_t scales[kFp8 ? kScaleUnits : 1];
+    __shared__ int arrived;
     extern __shared__ float part[];  // [kWaves][T][16]
-    for (int p = threadIdx.x; p < A.T * A.k; p += kThreads) L.ids[p] = A.ids[p];
+    static_assert(sizeof(Scratch) <= sizeof(stages), "the scratch fits the stages");
+    Scratch *W = reinterpret_cast<Scratch *>(stages);
+    for (int p = threadIdx.x; p < A.T * A.k; p += kThreads) {
+        W->ids[p] = A.ids[p];
+        weights[p] = A.weights[p];
+    }
     for (int i = threadIdx.x; i < kWaves * A.T * 16; i += kThreads) part[i] = 0.0f;
     __syncthreads();
-    build_lists(&L, A.T * A.k, A.gate.E);
-    const int wave = threadIdx.x / kWave, o0 = blockIdx.x * 16;
-    const int nw = windows_of<kFp8>(A.I), units = L.active * nw;
-    const int u1 = (int)((int64_t)units * (wave + 1) / kWaves);
-    float *mine = part + wave * A.T * 16;
-    for (int u = (int)((int64_t)units * wave / kWaves); u < u1;) {
-        const int a = u / nw, w0 = u - a * nw, w1 = min(nw, w0 + (u1 - u));
-        const int n = L.start[a + 1] - L.start[a];
-        if (n <= 16) down_run<kFp8, 1>(A, &L, a, o0, w0, w1, mine);
-        else if (n <= 32) down_run<kFp8, 2>(A, &L, a, o0, w0, w1, mine);
-        else down_run<kFp8, 4>(A, &L, a, o0, w0, w1, mine);
-        u += w1 - w0;
-        wave_lds_fence();  // the next expert adds to sums that other lanes wrote
+    build_lists<kCols>(&L, W, A.T, A.k, A.gate.E);
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = lane_id(), r = l & 15, q = l >> 4;
+    const int o0 = blockIdx.x * kRows, nw = windows_of<kFp8>(A.I);
+    const int64_t every = (int64_t)L.entries * nw;
+    const int u0 = (int)(every * blockIdx.y / gridDim.y), units = (int)(every * (blockIdx.y + 1) / gridDim.y) - u0;
+    if (units > 0) {
+        const bool partial = A.I % (64 * R::kHalves) != 0;
+        R ring;
+        ring.lds = stages;
+        ring.wave = wave;
+        ring.K = A.I;
+        int pu = 0, pa = u0 / nw, pwin = u0 - pa * nw;
+        auto sources = [&] {
+            const int e = L.expert[pa], first = L.start[pa];
+            const int n = ring.n = __builtin_amdgcn_readfirstlane(L.count[pa]);
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const int o = min(o0 + ring.weight_row(i), A.H - 1);
+                ring.w[i] = A.wd.data + e * A.wd.stride + o * row_bytes<kFp8>(A.I) + R::chunk() * 16;
+            }
+#pragma unroll
+            for (int i = 0; i < R::kMine; i++) {
+                const int c = ring.column_row(i) % kCols, ph = ring.column_row(i) / kCols;
+                const uint16_t *h = ph / R::kHalves ? A.hlo : A.hhi;
+                h += (int64_t)L.pair[first + min(c, n - 1)] * A.I;  // columns past the end repeat the last
+                ring.col[i] = reinterpret_cast<const uint8_t *>(h) + (ph % R::kHalves) * 128 + R::chunk() * 16;
+            }
+        };
+        auto produce = [&](int slot) {
+            ring.issue(slot, pwin, partial);
+            pu++;
+            if (pu < units && ++pwin == nw) {
+                pwin = 0;
+                pa++;
+                sources();
+            }
+        };
+        sources();
+#pragma unroll
+        for (int s = 0; s < R::kStages - 1; s++) produce(s);
+
+        f32x4 acc[R::kTiles];
+#pragma unroll
+        for (int t = 0; t < R::kTiles; t++) acc[t] = f32x4{0, 0, 0, 0};
+        int slot = 0, a = u0 / nw, win = u0 - a * nw;
+        float *mine = part + wave * A.T * 16;
+        for (int u = 0; u < units; u++) {
+            if (kFp8 && u % kScaleUnits == 0) {
+                if (u > 0) __syncthreads();
+                for (int i = threadIdx.x; i < min(kScaleUnits, units - u); i += kThreads) {
+                    const int un = u0 + u + i, e = L.expert[un / nw];
+                    scales[i] = A.wd.scale[e * A.wd.scale_stride + (int64_t)(o0 / kScaleBlock) * nw + un % nw];
+                }
+            }
+            ring.arrive();
+            produce(slot == 0 ? R::kStages - 1 : slot - 1);
+            const int n = __builtin_amdgcn_readfirstlane(L.count[a]);
+            float scale = 1.0f;
+            if constexpr (kFp8) scale = pow2_of(scales[u % kScaleUnits]);
+            ring.multiply(slot, n, scale, acc);
+            slot = slot == R::kStages - 1 ? 0 : slot + 1;
+            if (++win < nw && u + 1 < units) continue;
+            // the wave's own sums: an entry has a token once, so lanes do not meet
+#pragma unroll
+            for (int t = 0; t < R::kTiles; t++) {
+                if (t * 8 >= n) break;
+                f32x4 both;
+#pragma unroll
+                for (int i = 0; i < 4; i++) both[i] = acc[t][i] + __shfl_xor(acc[t][i], 8);
+                const int c = t * 8 + r;
+                if (r < 8 && c < n) {
+                    const int p = L.pair[L.start[a] + c];
+                    f32x4 *d = reinterpret_cast<f32x4 *>(mine + (p / A.k) * 16 + 4 * q);
+                    f32x4 v = *d;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) v[i] += weights[p] * both[i];
+                    *d = v;
+                }
+                acc[t] = f32x4{0, 0, 0, 0};
+            }
+            wave_lds_fence();  // the next entry adds to sums that other lanes wrote
+            win = 0;
+            a++;
+        }
+        wait_loads();  // those that nobody reads
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < A.T * 16; i += kThreads) {
-        const int t = i / 16, o = o0 + i % 16;
-        if (o >= A.H) continue;
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; w++) s += part[w * A.T * 16 + i];
-        A.out[t * A.out_stride + o] = to_bf16(s);
+    const int rows = min(kRows, A.H - o0);
+    auto value = [&](int t, int o) { return part[(o / 16 * A.T + t) * 16 + o % 16]; };
+    if (gridDim.y == 1) {
+        for (int i = threadIdx.x; i < A.T * rows; i += kThreads) {
+            const int t = i / rows, o = i - t * rows;
+            A.out[t * A.out_stride + o0 + o] = to_bf16(value(t, o));
+        }
+        return;
     }
+    // Shares meet in memory: each writes its sums, and the last of a block of
+    // rows to arrive adds them in the shares' order.  The sums are written and
+    // read past the L2s, which the XCDs do not share (relaxed atomics of device
+    // scope), so that waiting for the stores orders them before the arrival; a
+    // fence would write back a whole L2 from every workgroup (70 us measured).
+    // Four outputs a thread at a time (rows and H are multiples of 8).
+    float *sums = A.sums + o0;
+    const int64_t share = (int64_t)A.T * A.H;
+    const int quads = rows / 4;
+    for (int i = threadIdx.x; i < A.T * quads; i += kThreads) {
+        const int t = i / quads, o = (i - t * quads) * 4;
+        uint64_t *p = reinterpret_cast<uint64_t *>(sums + blockIdx.y * share + (int64_t)t * A.H + o);
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(part + (o / 16 * A.T + t) * 16 + o % 16);
+        store_past_l2(p, v[0], v[1]);
+        store_past_l2(p + 1, v[2], v[3]);
+    }
+    wait_loads();  // stores count too
+    __syncthreads();
+    if (threadIdx.x == 0)
+        arrived = __hip_atomic_fetch_add(A.arrivals + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != (int)gridDim.y - 1) return;
+    for (int i = threadIdx.x; i < A.T * quads; i += kThreads) {
+        const int t = i / quads, o = (i - t * quads) * 4;
+        const uint64_t *p = reinterpret_cast<const uint64_t *>(sums + (int64_t)t * A.H + o);
+        float v[4] = {0, 0, 0, 0};
+        for (int s0 = 0; s0 < (int)gridDim.y; s0 += 8) {
+            uint64_t f[8][2];  // 16 loads in flight
+#pragma unroll
+            for (int s = 0; s < 8; s++)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    f[s][h] = s0 + s < (int)gridDim.y
+                                  ? __hip_atomic_load(p + (s0 + s) * (share / 2) + h, __ATOMIC_RELAXED,
+                                                      __HIP_MEMORY_SCOPE_AGENT)
+                                  : 0;
+#pragma unroll
+            for (int s = 0; s < 8; s++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    v[2 * h] += __builtin_bit_cast(float, (uint32_t)f[s][h]);
+                    v[2 * h + 1] += __builtin_bit_cast(float, (uint32_t)(f[s][h] >> 32));
+                }
+        }
+        uint16_t *out = A.out + t * A.out_stride + o0 + o;
+#pragma unroll
+        for (int j = 0; j < 4; j++) out[j] = to_bf16(v[j]);
+    }
+}
+
+template <bool kFp8, int kCols>
+const void *up_function(int E) {
+    const int per = (E + kGateLanes - 1) / kGateLanes;
+    return per <= 8    ? (const void *)up_kernel<kFp8, kCols, 8>
+           : per <= 16 ? (const void *)up_kernel<kFp8, kCols, 16>
+           : per <= 24 ? (const void *)up_kernel<kFp8, kCols, 24>
+           : per <= 32 ? (const void *)up_kernel<kFp8, kCols, 32>
+                       : (const void *)up_kernel<kFp8, kCols, 64>;
+}
+
+template <bool kFp8, int kUpCols, int kDownCols>
+hipError_t launch(const FewArgs &A, hipStream_t s) {
+    const int64_t most = ((int64_t)(A.gate.E < A.T * A.k ? A.gate.E : A.T * A.k) + A.T * A.k / kUpCols) *
+                         ceil_div(A.I, kUpRows);
+    const void *up = up_function<kFp8, kUpCols>(A.gate.E);
+    const int64_t resident = resident_blocks(up, kThreads, 0);
+    const int64_t blocks = resident > 0 && resident < most ? resident : most;
+    void *args[] = {const_cast<FewArgs *>(&A)};
+    const hipError_t e = hipLaunchKernel(up, dim3((uint32_t)blocks), dim3(kThreads), args, 0, s);
+    if (e != hipSuccess) return e;
+    return hipLaunchKernel((const void *)down_kernel<kFp8, kDownCols>,
+                           dim3((uint32_t)ceil_div(A.H, kRows), down_shares(A.T, A.k, A.H, A.I)), dim3(kThreads), args,
+                           (size_t)kWaves * A.T * 16 * sizeof(float), s);
 }
 
 template <bool kFp8>
 hipError_t launch(const FewArgs &A, hipStream_t s) {
-    const int64_t most = (int64_t)(A.gate.E < A.T * A.k ? A.gate.E : A.T * A.k) * ((A.I + 7) / 8);
-    const int per = (A.gate.E + kGateLanes - 1) / kGateLanes;
-    const void *fn = per <= 8    ? (const void *)up_kernel<kFp8, 8>
-                     : per <= 16 ? (const void *)up_kernel<kFp8, 16>
-                     : per <= 24 ? (const void *)up_kernel<kFp8, 24>
-                     : per <= 32 ? (const void *)up_kernel<kFp8, 32>
-                                 : (const void *)up_kernel<kFp8, 64>;
-    const int64_t resident = resident_blocks(fn, kThreads, 0);
-    const int64_t blocks = resident > 0 && resident < most ? resident : most;
-    void *args[] = {const_cast<FewArgs *>(&A)};
-    hipError_t e = hipLaunchKernel(fn, dim3((uint32_t)blocks), dim3(kThreads), args, 0, s);
-    if (e != hipSuccess) return e;
-    down_kernel<kFp8><<<(uint32_t)ceil_div(A.H, 16), kThreads, (size_t)kWaves * A.T * 16 * sizeof(float), s>>>(A);
-    return hipGetLastError();
+    // a token takes an expert once: with 8 tokens no expert has more than 8 pairs
+    return A.T <= kFew ? launch<kFp8, kFew, kFew>(A, s) : launch<kFp8, kUpMany, kDownMany>(A, s);
 }
 
 // one expert matrix [rows][K]: pointers, alignment and strides that hold it
@@ -368,18 +595,41 @@ Matrix matrix_of(const ep_matrix_t &m) {
 
 using namespace ep;
 
-extern "C" size_t ep_few_tokens_workspace_bytes(int32_t num_tokens, int32_t top_k, int32_t inter) {
-    if (num_tokens < 0 || num_tokens > kMaxTokens || top_k < 1 || top_k > kGateMaxK || inter < 1) return 0;
-    return (size_t)num_tokens * top_k * inter * 2 * sizeof(uint16_t);
+namespace {
+
+// Parts of the workspace, in bytes from its start
+struct Parts {
+    size_t low, arrivals, sums, total;
+};
+
+Parts parts_of(int32_t T, int32_t k, int32_t H, int32_t I) {
+    Parts p;
+    p.low = (size_t)T * k * I * sizeof(uint16_t);  // a multiple of 16: I is one of 8
+    p.arrivals = align256(2 * p.low);
+    p.sums = p.arrivals + align256((size_t)ceil_div(H, kRows) * sizeof(int32_t));
+    p.total = p.sums + (size_t)down_shares(T, k, H, I) * T * H * sizeof(float);
+    return p;
+}
+
+bool sizes_ok(int32_t T, int32_t k, int32_t H, int32_t I) {
+    return T >= 0 && T <= kMaxTokens && k >= 1 && k <= kGateMaxK && H >= 8 && I >= 8 && H % 8 == 0 && I % 8 == 0 &&
+           H <= kMaxWidth && I <= kMaxWidth;
+}
+
+}  // namespace
+
+extern "C" size_t ep_few_tokens_workspace_bytes(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t inter) {
+    if (!sizes_ok(num_tokens, top_k, hidden, inter) || num_tokens == 0) return 0;
+    return parts_of(num_tokens, top_k, hidden, inter).total;
 }
 
 extern "C" int ep_moe_few_tokens(const void *x, int64_t x_stride, int32_t num_tokens, const void *logits,
                                  int64_t logits_stride, const ep_gate_t *gate, const ep_experts_t *experts, void *out,
                                  int64_t out_stride, int32_t *ids, float *weights, void *ws, size_t ws_bytes,
                                  ep_stream_t stream) {
-    if (!gate_ok(gate) || !experts || num_tokens < 0 || num_tokens > kMaxTokens) return EP_ERR_INVALID_ARG;
+    if (!gate_ok(gate) || !experts || !sizes_ok(num_tokens, gate->top_k, experts->hidden, experts->inter))
+        return EP_ERR_INVALID_ARG;
     const int32_t H = experts->hidden, I = experts->inter, E = gate->num_experts;
-    if (H < 8 || I < 8 || H % 8 != 0 || I % 8 != 0 || H > (1 << 20) || I > (1 << 20)) return EP_ERR_INVALID_ARG;
     if (experts->dtype != EP_DTYPE_BF16 && experts->dtype != EP_DTYPE_FP8) return EP_ERR_INVALID_ARG;
     const bool fp8 = experts->dtype == EP_DTYPE_FP8;
     if (!matrix_ok(experts->gate, fp8, I, H, E) || !matrix_ok(experts->up, fp8, I, H, E) ||
@@ -391,8 +641,8 @@ extern "C" int ep_moe_few_tokens(const void *x, int64_t x_stride, int32_t num_to
     if (!x || !logits || !out || !ids || !weights || !is_aligned(x, 16) || !is_aligned(logits, width) ||
         !is_aligned(out, 2) || !is_aligned(ids, 4) || !is_aligned(weights, 4))
         return EP_ERR_INVALID_ARG;
-    if (!ws || !is_aligned(ws, 16) || ws_bytes < ep_few_tokens_workspace_bytes(num_tokens, gate->top_k, I))
-        return EP_ERR_INVALID_ARG;
+    const Parts parts = parts_of(num_tokens, gate->top_k, H, I);
+    if (!ws || !is_aligned(ws, 16) || ws_bytes < parts.total) return EP_ERR_INVALID_ARG;
     FewArgs A;
     A.gate = gate_args(logits, logits_stride, gate);
     A.x = static_cast<const uint16_t *>(x);
@@ -408,7 +658,10 @@ extern "C" int ep_moe_few_tokens(const void *x, int64_t x_stride, int32_t num_to
     A.ids = ids;
     A.weights = weights;
     A.out = static_cast<uint16_t *>(out);
-    A.hhi = static_cast<uint16_t *>(ws);
-    A.hlo = A.hhi + (size_t)num_tokens * gate->top_k * I;
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    A.hhi = reinterpret_cast<uint16_t *>(w);
+    A.hlo = reinterpret_cast<uint16_t *>(w + parts.low);
+    A.arrivals = reinterpret_cast<int32_t *>(w + parts.arrivals);
+    A.sums = reinterpret_cast<float *>(w + parts.sums);
     return rc_of(fp8 ? launch<true>(A, to_stream(stream)) : launch<false>(A, to_stream(stream)));
 }

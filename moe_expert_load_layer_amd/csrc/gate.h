@@ -6,10 +6,12 @@
 //   chosen the k largest s, equal ones by lowest expert
 //   weight w_j = scale * exp(l_j - max l) / sum_i exp(l_i - max l) over the chosen
 //
-// Lane i holds the V consecutive experts from i * V on, so that among equal
-// scores the lowest lane, and in it the lowest register, is the lowest expert.
-// k rounds: the lanes' maxima meet in 4 DPP steps, a ballot names the lowest
-// lane that has it, and that lane drops the value.
+// Lane i holds the experts of the chunks of 8 with numbers i, i + 16, ...  The
+// lanes' maxima are ranked by rotating them round the row; the k-th of them, tau,
+// is a lower bound of the k-th largest score, so only scores from tau on (11 or
+// so of 384 for k = 8) are candidates.  They go to LDS, and each counts those
+// before it.  Where masks or ties leave more than 32 candidates, k rounds of a
+// maximum over the row choose instead.  The choice is the same either way.
 #pragma once
 
 #include "layer.h"
@@ -29,13 +31,21 @@ struct GateArgs {
     float scale;
     int32_t bf16;  // the logits' type
     int32_t vec;   // rows start on 16 bytes
+    int32_t bias_vec;
 };
+
+constexpr int kGateCandidates = 2 * kGateLanes;
 
 // LDS of one token
 struct GateSlot {
     int32_t chosen[kGateMaxK];
     uint32_t group[kGateMaxGroups];
+    float score[kGateCandidates];
+    int32_t expert[kGateCandidates];
 };
+
+// expert of register i of a lane
+__device__ __forceinline__ int gate_expert(int lane, int i) { return ((i / 8) * kGateLanes + lane) * 8 + i % 8; }
 
 // unsigned order of floats
 __device__ __forceinline__ uint32_t float_order(float f) {
@@ -51,10 +61,9 @@ __device__ __forceinline__ float gate_logit(const GateArgs &A, int64_t t, int e)
 
 template <int V>
 __device__ __forceinline__ void gate_scores(const GateArgs &A, int64_t t, int lane, float (&v)[V]) {
-    const int e0 = lane * V;
 #pragma unroll
     for (int i = 0; i < V; i += 8) {
-        const int e = e0 + i;
+        const int e = gate_expert(lane, i);
         if (A.vec && e + 8 <= A.E) {
             if (A.bf16) {
                 const u32x4 w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(A.logits) +
@@ -78,11 +87,27 @@ __device__ __forceinline__ void gate_scores(const GateArgs &A, int64_t t, int la
             for (int j = 0; j < 8; j++) v[i + j] = e + j < A.E ? gate_logit(A, t, e + j) : -INFINITY;
         }
     }
+    if (A.bias) {
+#pragma unroll
+        for (int i = 0; i < V; i += 8) {
+            const int e = gate_expert(lane, i);
+            if (A.bias_vec && e + 8 <= A.E) {
+                const f32x4 *p = reinterpret_cast<const f32x4 *>(A.bias + e);
+                const f32x4 a = p[0], b = p[1];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    v[i + j] += a[j];
+                    v[i + 4 + j] += b[j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++) v[i + j] += e + j < A.E ? A.bias[e + j] : 0.0f;
+            }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        float s = v[i];
-        if (A.bias && e0 + i < A.E) s += A.bias[e0 + i];
-        s += 0.0f;  // -0 and 0 are equal scores
+        const float s = v[i] + 0.0f;  // -0 and 0 are equal scores
         v[i] = s == s ? s : -INFINITY;
     }
 }
@@ -90,21 +115,24 @@ __device__ __forceinline__ void gate_scores(const GateArgs &A, int64_t t, int la
 // Drops the scores outside the best groups.
 template <int V>
 __device__ __forceinline__ void gate_groups(const GateArgs &A, int lane, GateSlot *slot, float (&v)[V]) {
-    const int gs = A.E / A.G, e0 = lane * V;
+    const int gs = A.E / A.G;
     slot->group[lane] = 0;
     wave_lds_fence();
-    {
+    // a chunk's 8 experts are consecutive: their maxima go out group by group
+#pragma unroll
+    for (int i = 0; i < V; i += 8) {
+        const int e0 = gate_expert(lane, i);
         int g = e0 / gs, next = (g + 1) * gs;
         float best = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            if (e0 + i == next) {
+        for (int j = 0; j < 8; j++) {
+            if (e0 + j == next) {
                 if (g < A.G) atomicMax(&slot->group[g], float_order(best));
                 best = -INFINITY;
                 g++;
                 next += gs;
             }
-            best = fmaxf(best, v[i]);
+            best = fmaxf(best, v[i + j]);
         }
         if (g < A.G) atomicMax(&slot->group[g], float_order(best));
     }
@@ -117,14 +145,58 @@ __device__ __forceinline__ void gate_groups(const GateArgs &A, int lane, GateSlo
     }
     const uint64_t all = __ballot(lane < A.G && rank < A.TG);
     const uint32_t keep = (uint32_t)(all >> (lane_id() & ~(kGateLanes - 1))) & 0xffffu;
-    int g = e0 / gs, next = (g + 1) * gs;
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        if (e0 + i == next) {
-            g++;
-            next += gs;
+    for (int i = 0; i < V; i += 8) {
+        const int e0 = gate_expert(lane, i);
+        int g = e0 / gs, next = (g + 1) * gs;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            if (e0 + j == next) {
+                g++;
+                next += gs;
+            }
+            if (!((keep >> (g & 31)) & 1u)) v[i + j] = -INFINITY;
         }
-        if (!((keep >> (g & 31)) & 1u)) v[i] = -INFINITY;
+    }
+}
+
+// lanes of the row whose value is greater, by rotating the row's values
+template <int kStep>
+__device__ __forceinline__ int row_greater(float v) {
+    if constexpr (kStep == kGateLanes) return 0;
+    else return (dpp_f32<0x120 + kStep>(v) > v ? 1 : 0) + row_greater<kStep + 1>(v);
+}
+
+__device__ __forceinline__ int row_min_i32(int v) {
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true));
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true));
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));
+    return min(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true));
+}
+
+// inclusive prefix sum over the row of 16 (row_shr fills zeros from the left)
+__device__ __forceinline__ int row_scan_i32(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    return v + __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+}
+
+// k rounds of the row's maximum, the lowest expert among equal ones; v is used up
+template <int V>
+__device__ __forceinline__ void gate_rounds(const GateArgs &A, int lane, GateSlot *slot, float (&v)[V]) {
+    for (int j = 0; j < A.k; j++) {
+        float best = v[0];
+#pragma unroll
+        for (int i = 1; i < V; i++) best = fmaxf(best, v[i]);
+        const float top = row_max_f32(best);
+        int e = INT32_MAX;
+#pragma unroll
+        for (int i = V - 1; i >= 0; i--) e = v[i] == top ? gate_expert(lane, i) : e;  // ascending in i
+        const int first = row_min_i32(e);
+        slot->chosen[j] = top > -INFINITY ? first : -1;  // every lane of the row writes the same
+#pragma unroll
+        for (int i = 0; i < V; i++) v[i] = gate_expert(lane, i) == first ? -INFINITY : v[i];
     }
 }
 
@@ -136,23 +208,48 @@ __device__ __forceinline__ void gate_token(const GateArgs &A, int64_t t, GateSlo
     float v[V];
     gate_scores<V>(A, t, lane, v);
     if (A.G > 1) gate_groups<V>(A, lane, slot, v);
-    for (int j = 0; j < A.k; j++) {
-        float best = v[0];
+    float best = v[0];
 #pragma unroll
-        for (int i = 1; i < V; i++) best = fmaxf(best, v[i]);
-        const float top = row_max_f32(best);
-        const bool has = best == top && top > -INFINITY;
-        const uint64_t all = __ballot(has);
-        const uint32_t row = (uint32_t)(all >> (lane_id() & ~(kGateLanes - 1))) & 0xffffu;
-        const bool win = has && (row & ((1u << lane) - 1)) == 0;
-        int at = -1;
+    for (int i = 1; i < V; i++) best = fmaxf(best, v[i]);
+    // at least k lanes have fewer than k greater maxima, so k scores at least
+    // are not below the least of those maxima
+    const float tau = -row_max_f32(row_greater<1>(best) < A.k ? -best : -INFINITY);
+    int mine = 0;
 #pragma unroll
-        for (int i = V - 1; i >= 0; i--) at = v[i] == top ? i : at;
-        if (win) slot->chosen[j] = lane * V + at;
-        if (row == 0) slot->chosen[j] = -1;  // every lane of the row writes the same
-        at = win ? at : -1;
+    for (int i = 0; i < V; i++) mine += v[i] >= tau && v[i] > -INFINITY;
+    const int upto = row_scan_i32(mine);
+    const int n = __shfl(upto, lane_id() | (kGateLanes - 1));
+    if (__any(n > kGateCandidates)) {
+        gate_rounds<V>(A, lane, slot, v);
+    } else {
+        slot->chosen[lane] = -1;
+        int at = upto - mine;
 #pragma unroll
-        for (int i = 0; i < V; i++) v[i] = i == at ? -INFINITY : v[i];
+        for (int i = 0; i < V; i++)
+            if (v[i] >= tau && v[i] > -INFINITY) {
+                slot->score[at] = v[i];
+                slot->expert[at] = gate_expert(lane, i);
+                at++;
+            }
+        wave_lds_fence();
+        float s[2];
+        int e[2], before[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            s[c] = slot->score[lane + c * kGateLanes];  // past the n-th: not used
+            e[c] = slot->expert[lane + c * kGateLanes];
+        }
+#pragma unroll 4
+        for (int o = 0; o < n; o++) {
+            const float so = slot->score[o];
+            const int eo = slot->expert[o];
+#pragma unroll
+            for (int c = 0; c < 2; c++) before[c] += so > s[c] || (so == s[c] && eo < e[c]);
+        }
+        wave_lds_fence();
+#pragma unroll
+        for (int c = 0; c < 2; c++)
+            if (lane + c * kGateLanes < n && before[c] < A.k) slot->chosen[before[c]] = e[c];
     }
     wave_lds_fence();
     id = lane < A.k ? slot->chosen[lane] : -1;

@@ -28,6 +28,7 @@ GateArgs gate_args(const void *logits, int64_t stride, const ep_gate_t *g) {
     A.scale = g->scale;
     A.bf16 = g->logits_dtype == EP_DTYPE_BF16;
     A.vec = is_aligned(logits, 16) && (stride * width) % 16 == 0;
+    A.bias_vec = is_aligned(g->bias, 16);
     return A;
 }
 

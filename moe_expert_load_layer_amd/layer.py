@@ -70,7 +70,7 @@ def declare(L: ctypes.CDLL) -> None:
     L.ep_grouped_matmul.argtypes = [p(_CMatmul), _vp]
     L.ep_grouped_wgrad.argtypes = [p(_CWgrad), _vp]
     L.ep_moe_combine.argtypes = [_vp, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _vp]
-    L.ep_few_tokens_workspace_bytes.argtypes = [_i32, _i32, _i32]
+    L.ep_few_tokens_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32]
     L.ep_few_tokens_workspace_bytes.restype = _sz
     L.ep_moe_few_tokens.argtypes = [_vp, _i64, _i32, _vp, _i64, p(_CGate), p(_CExperts), _vp, _i64, _vp, _vp, _vp,
                                     _sz, _vp]
@@ -315,8 +315,8 @@ def ep_moe_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, ou
     return out
 
 
-def ep_few_tokens_workspace_bytes(num_tokens: int, top_k: int, inter: int) -> int:
-    return int(lib().ep_few_tokens_workspace_bytes(int(num_tokens), int(top_k), int(inter)))
+def ep_few_tokens_workspace_bytes(num_tokens: int, top_k: int, hidden: int, inter: int) -> int:
+    return int(lib().ep_few_tokens_workspace_bytes(int(num_tokens), int(top_k), int(hidden), int(inter)))
 
 
 def ep_moe_few_tokens(x: torch.Tensor, logits: torch.Tensor, k: int, gate: torch.Tensor, up: torch.Tensor,
@@ -326,7 +326,7 @@ def ep_moe_few_tokens(x: torch.Tensor, logits: torch.Tensor, k: int, gate: torch
     """The whole layer for at most EP_MAX_FEW_TOKENS tokens -> (out bf16 [T][H], ids int32 [T][k], weights [T][k]).
 
     x bf16 [T][H], logits [T][E] as for ep_gate_topk, gate and up [E][I][H], down [E][H][I] in bf16 or, with the
-    scales of ep_quant_blocks, in 8 bits.  ws: ep_few_tokens_workspace_bytes(T, k, I) bytes."""
+    scales of ep_quant_blocks, in 8 bits.  ws: ep_few_tokens_workspace_bytes(T, k, H, I) bytes."""
     xs = _rows(x, (torch.bfloat16,), "x")
     ls = _rows(logits, (torch.float32, torch.bfloat16), "logits")
     (T, H), E = x.shape, logits.shape[1]
@@ -348,7 +348,7 @@ def ep_moe_few_tokens(x: torch.Tensor, logits: torch.Tensor, k: int, gate: torch
     weights = _out(weights, torch.float32, (T, k), x.device, "weights")
     g = _gate(E, k, bias, num_groups, topk_groups, scale, logits.dtype)
     if ws is None:
-        ws = torch.empty(max(16, ep_few_tokens_workspace_bytes(T, k, I)), dtype=torch.uint8, device=x.device)
+        ws = torch.empty(max(16, ep_few_tokens_workspace_bytes(T, k, H, I)), dtype=torch.uint8, device=x.device)
     elif not (ws.is_cuda and ws.is_contiguous()):
         raise EPBalanceError("ws must be a contiguous device tensor")
     rc = lib().ep_moe_few_tokens(_ptr(x), xs, T, _ptr(logits), ls, ctypes.byref(g), ctypes.byref(e), _ptr(out), H,

@@ -86,7 +86,7 @@ def test_layer_packed_rows_strides_and_workspace(dev):
     x = torch.from_numpy(rng.normal(0, 1, (T, 2 * H)).astype(np.float32)).to(torch.bfloat16).to(dev)[:, H:]
     logits = torch.from_numpy(rng.normal(0, 1, (T, E + 3)).astype(np.float32)).to(dev)[:, 1:E + 1]
     a = ep.ep_moe_few_tokens(x, logits, k, g, u, d)
-    ws = torch.full((ep.ep_few_tokens_workspace_bytes(T, k, I),), 255, dtype=torch.uint8, device=dev)
+    ws = torch.full((ep.ep_few_tokens_workspace_bytes(T, k, H, I),), 255, dtype=torch.uint8, device=dev)
     outs = (torch.full((T, H), 9.0, dtype=torch.bfloat16, device=dev),
             torch.full((T, k), 9, dtype=torch.int32, device=dev), torch.full((T, k), 9.0, device=dev))
     b = ep.ep_moe_few_tokens(x.contiguous(), logits.contiguous(), k, g.contiguous(), u.contiguous(), d.contiguous(),
