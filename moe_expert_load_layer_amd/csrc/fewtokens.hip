@@ -138,7 +138,7 @@ __device__ __forceinline__ int64_t row_bytes(int K) {
 
 // Waits until at most n of this wave's loads are in flight; n is the same in
 // every lane.  The instruction's count is a constant, hence the cases.
-__device__ __forceinline__ void wait_loads_but(int n) {
+__device__ __forceinline__ void wait_loads_but_n(int n) {
     switch (n) {
 #define EP_WAIT(N) \
     case N: asm volatile("s_waitcnt vmcnt(" #N ")" ::: "memory"); break;
@@ -199,7 +199,7 @@ struct Ring {
     // waits until all but the newest window's loads are there
     __device__ __forceinline__ void arrive() const {
         static_assert(kStages == 3 && 2 + kMine <= 6, "one window stays in flight, its loads have a case");
-        wait_loads_but(flying);
+        wait_loads_but_n(flying);
         __syncthreads();
     }
 

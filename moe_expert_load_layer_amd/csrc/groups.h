@@ -88,6 +88,12 @@ __device__ __forceinline__ void load_lds_1k(const void *g, void *lds) {
 }
 #pragma clang diagnostic pop
 
+// Waits until at most N of this wave's loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads_but() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 }  // namespace ep

@@ -22,6 +22,11 @@
 namespace ep {
 namespace {
 
+#ifndef EP_BIG
+#define EP_BIG 256, 256, 64, 128, 2
+#define EP_S2 2
+#define EP_S3 3
+#endif
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct MatmulArgs {
@@ -38,10 +43,16 @@ struct MatmulArgs {
     uint16_t *y;
 };
 
+// A K step is a block of 128 values; LDS rows are its 128 bytes, their 16-byte
+// chunks exchanged by the row's bits 1 to 3: 16 lanes reading one chunk of 16
+// rows (256 bytes, a cycle's worth) meet every bank once.
+constexpr int kStep = 128;
+__device__ __forceinline__ int exchange(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+
 // 32 bytes of LDS row r from chunk c on (c even)
 __device__ __forceinline__ i32x8 read_frag(const uint8_t *tile, int r, int c) {
-    const u32x4 a = *reinterpret_cast<const u32x4 *>(tile + r * 128 + ((c ^ (r & 7)) << 4));
-    const u32x4 b = *reinterpret_cast<const u32x4 *>(tile + r * 128 + (((c + 1) ^ (r & 7)) << 4));
+    const u32x4 a = *reinterpret_cast<const u32x4 *>(tile + r * kStep + (exchange(r, c) << 4));
+    const u32x4 b = *reinterpret_cast<const u32x4 *>(tile + r * kStep + (exchange(r, c + 1) << 4));
     i32x8 f;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -51,26 +62,20 @@ __device__ __forceinline__ i32x8 read_frag(const uint8_t *tile, int r, int c) {
     return f;
 }
 
-// One K step of a wave: starts the loads of the next stage and multiplies this
-// one.  The stages are restrict pointers so that the reads of one do not wait
-// for the loads into the other.  ahead: how far the sources move (0 at the end:
-// the last block is fetched again rather than branched around).  xs: scale bytes of the step, one a row of x
-// (kScaleRow bytes apart), ws: the scale byte of the wave's weights.
-constexpr int kScaleBlocks = 64;               // blocks whose scales are in LDS at a time
-constexpr int kScaleRow = kScaleBlocks + 4;    // rows 17 banks apart
+constexpr int kScaleBlocks = 32;             // blocks whose scales are in LDS at a time
+constexpr int kScaleRow = kScaleBlocks + 4;  // rows 9 banks apart
 
+// One K step of a wave: starts the loads of a later stage and multiplies this
+// one.  ahead: how far the sources move (0 at the end: the last step is fetched
+// again, so that every step has the same count of loads).  xs: scale bytes of
+// the block, one a row of x (kScaleRow bytes apart), ws: the scale byte of the
+// wave's weights.
 template <int BM, int FM, int FN, int kLoads, int kWaves>
-__device__ __forceinline__ void matmul_step(const uint8_t *__restrict__ cur, uint8_t *__restrict__ next,
-                                            const uint8_t *(&src)[kLoads], int ahead, int wave, int xrow, int wrow,
-                                            const uint8_t *__restrict__ xs, const uint8_t *__restrict__ ws,
-                                            f32x16 (&acc)[FN][FM]) {
+__device__ __forceinline__ void matmul_step(const uint8_t *cur, uint8_t *next, const uint8_t *(&src)[kLoads],
+                                            int ahead, int wave, int xrow, int wrow, const uint8_t *xs,
+                                            const uint8_t *ws, f32x16 (&acc)[FN][FM]) {
     const int l = lane_id(), r = l & 31, h = l >> 5;
-#pragma unroll
-    for (int i = 0; i < kLoads; i++) {
-        load_lds_1k(src[i], next + (wave + i * kWaves) * 1024);
-        src[i] += ahead;
-    }
-    const uint8_t *tx = cur + xrow * 128, *tw = cur + (BM + wrow) * 128;
+    const uint8_t *tx = cur + xrow * kStep, *tw = cur + (BM + wrow) * kStep;
     int sx[FM];
 #pragma unroll
     for (int j = 0; j < FM; j++) sx[j] = xs[(xrow + j * 32 + r) * kScaleRow];
@@ -83,24 +88,33 @@ __device__ __forceinline__ void matmul_step(const uint8_t *__restrict__ cur, uin
 #pragma unroll
         for (int i = 0; i < FN; i++) fw[i] = read_frag(tw, i * 32 + r, s * 4 + h * 2);
 #pragma unroll
-        for (int i = 0; i < FN; i++)
+        for (int i = 0; i < FN; i++) {
 #pragma unroll
             for (int j = 0; j < FM; j++)
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[i], fx[j], acc[i][j], 0, 0, 0, sw, 0,
                                                                             sx[j]);
+            // the loads go out between the products: at the step's start they
+            // would all wait for the address unit, and the products for them
+#pragma unroll
+            for (int p = (s * FN + i) * kLoads / (2 * FN); p < (s * FN + i + 1) * kLoads / (2 * FN); p++) {
+                load_lds_1k(src[p], next + (wave + p * kWaves) * 1024);
+                src[p] += ahead;
+            }
+        }
     }
 }
 
-template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave) void matmul_kernel(const MatmulArgs A) {
+template <int BM, int BN, int WM, int WN, int kStages>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kernel(const MatmulArgs A) {
     constexpr int kWavesM = BM / WM, kWaves = kWavesM * (BN / WN), kThreads = kWaves * kWave;
     constexpr int FM = WM / 32, FN = WN / 32;
     constexpr int kLoads = (BM + BN) / 8 / kWaves;  // 1 KiB loads of a wave in a step
-    constexpr int kStage = (BM + BN) * 128;
+    constexpr int kStage = (BM + BN) * kStep;
     constexpr int kWScales = (BN + kScaleBlock - 1) / kScaleBlock;
     static_assert((BM + BN) % (8 * kWaves) == 0 && BM % 8 == 0, "whole loads");
     static_assert(kScaleBlock % WN == 0, "a wave's columns share a scale");
-    __shared__ __align__(16) uint8_t stages[2 * kStage];
+    constexpr int kOut = BM * BN * 2, kRing = kStages * kStage;
+    __shared__ __align__(16) uint8_t stages[kRing > kOut ? kRing : kOut];
     __shared__ __align__(16) uint8_t scales[(BM + kWScales) * kScaleRow];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = lane_id();
@@ -152,7 +166,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave) void matmul_kernel(c
         const uint8_t *src[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; i++) {
-            const int r = (wave + i * kWaves) * 8 + l / 8, c = (l % 8) ^ (r & 7);
+            const int r = (wave + i * kWaves) * 8 + l / 8, c = exchange(r, l % 8);
             if (r < BM) {
                 const int s = source(min(m0 + r, m1 - 1));  // rows past the end repeat the last
                 src[i] = A.x + max(s, 0) * row_bytes + c * 16;
@@ -178,24 +192,31 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave) void matmul_kernel(c
                         ws[(int64_t)min(n0 / kScaleBlock + j, (A.N - 1) / kScaleBlock) * A.kb + b0 + b];
             }
         };
+        // steps go round the ring; kStages - 1 of them are in flight or being read
+        const int steps = A.kb;
 #pragma unroll
-        for (int i = 0; i < kLoads; i++) {
-            load_lds_1k(src[i], stages + (wave + i * kWaves) * 1024);
-            src[i] += A.kb > 1 ? 128 : 0;
-        }
+        for (int p = 0; p < kStages - 1; p++)
+#pragma unroll
+            for (int i = 0; i < kLoads; i++) {
+                load_lds_1k(src[i], stages + p * kStage + (wave + i * kWaves) * 1024);
+                src[i] += p + 1 < steps ? kStep : 0;
+            }
+        int slot = 0;
         for (int b0 = 0; b0 < A.kb; b0 += kScaleBlocks) {
             if (b0 > 0) __syncthreads();  // the scales before have been read
             scale_bytes(b0);
-            const int b1 = min(b0 + kScaleBlocks, A.kb);
-            for (int b = b0; b < b1; b++) {
+            const int s1 = min(b0 + kScaleBlocks, A.kb);
+            for (int s = b0; s < s1; s++) {
                 // this step's stage is complete once every wave's loads are, and
-                // the other stage has been read
-                wait_loads();
+                // the stage before has been read
+                wait_loads_but<(kStages - 2) * kLoads>();
                 __syncthreads();
-                const uint8_t *xs = scales + (b - b0);
-                matmul_step<BM, FM, FN, kLoads, kWaves>(stages + (b & 1) * kStage, stages + (~b & 1) * kStage, src,
-                                                        b + 2 < A.kb ? 128 : 0, wave, wm * WM, wn * WN, xs,
-                                                        xs + (BM + wn * WN / kScaleBlock) * kScaleRow, acc);
+                const uint8_t *xs = scales + (s - b0);
+                matmul_step<BM, FM, FN, kLoads, kWaves>(
+                    stages + slot * kStage, stages + (slot == 0 ? kStages - 1 : slot - 1) * kStage, src,
+                    s + kStages < steps ? kStep : 0, wave, wm * WM, wn * WN, xs,
+                    xs + (BM + wn * WN / kScaleBlock) * kScaleRow, acc);
+                slot = slot == kStages - 1 ? 0 : slot + 1;
             }
         }
         wait_loads();  // the load that nobody reads
@@ -206,7 +227,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave) void matmul_kernel(c
     // Chunks of 16 bytes are exchanged by the row, so that 32 rows written at one
     // column meet different banks.
     constexpr int kChunks = BN / 8;
-    static_assert(BM * BN * 2 <= 2 * kStage, "the tile fits the stages");
     uint16_t *out = reinterpret_cast<uint16_t *>(stages);
 #pragma unroll
     for (int j = 0; j < FM; j++) {
@@ -237,14 +257,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave) void matmul_kernel(c
     }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int kStages>
 hipError_t launch(const MatmulArgs &A, hipStream_t s) {
     constexpr int kThreads = (BM / WM) * (BN / WN) * kWave;
     // every group may end in a part tile, and so may the rows past the last
     const int64_t mt = A.groups.M / BM + A.groups.G + 1;
     const int64_t blocks = ceil_div(mt * ceil_div(A.N, BN), 8) * 8;
     if (blocks > 0xffffffffll / kThreads) return hipErrorInvalidConfiguration;
-    matmul_kernel<BM, BN, WM, WN><<<(uint32_t)blocks, kThreads, 0, s>>>(A);
+    matmul_kernel<BM, BN, WM, WN, kStages><<<(uint32_t)blocks, kThreads, 0, s>>>(A);
     return hipGetLastError();
 }
 
@@ -295,7 +315,7 @@ extern "C" int ep_grouped_matmul(const ep_grouped_matmul_t *p, ep_stream_t strea
     A.y = static_cast<uint16_t *>(p->y);
     const hipStream_t s = to_stream(stream);
     const int64_t rows = p->m / p->groups;  // of a group, on average
-    if (rows >= 384) return rc_of(launch<256, 256, 64, 128>(A, s));
-    if (rows >= 64) return rc_of(launch<128, 128, 64, 64>(A, s));
-    return rc_of(launch<32, 128, 32, 32>(A, s));
+    if (rows >= 384) return rc_of(launch<EP_BIG>(A, s));
+    if (rows >= 64) return rc_of(launch<128, 128, 64, 64, EP_S2>(A, s));
+    return rc_of(launch<32, 128, 32, 32, EP_S3>(A, s));
 }

@@ -37,13 +37,17 @@ struct WgradArgs {
     bool vec;                             // 16-byte rows and stores
 };
 
-constexpr int kRows = 64;  // rows of a step
+constexpr int kRows = 32;              // rows of a step
+constexpr int kTileK = 256, kTileN = 128;  // columns of x and of dy
+constexpr int kWaveK = 128, kWaveN = 64;
+constexpr int kWavesK = kTileK / kWaveK, kWaves = kWavesK * (kTileN / kWaveN), kThreads = kWaves * kWave;
+constexpr int kStages = 3;
 
-// the chunk of an LDS row that holds chunk c of the matrix row
-__device__ __forceinline__ int swizzle(int row, int c) { return c ^ (((row & 3) << 1) | (row & 8)); }
+// the 16-byte chunk of an LDS row that holds chunk c of the matrix row
+__device__ __forceinline__ int swizzle(int row, int c) { return c ^ ((row & 3) << 2); }
 
 // rows t .. t + 7 (this lane's half of 16) of column c0 + l % 32, as 8 bf16
-template <int BC>
+template <int kCols>
 __device__ __forceinline__ bf16x8 read_columns(const uint16_t *tile, int t0, int c0) {
     const int l = lane_id(), i = l & 15, c = c0 + ((l >> 4) & 1) * 16 + (i & 3) * 4;
     union {
@@ -53,31 +57,70 @@ __device__ __forceinline__ bf16x8 read_columns(const uint16_t *tile, int t0, int
 #pragma unroll
     for (int p = 0; p < 2; p++) {
         const int t = t0 + (l >> 5) * 8 + p * 4 + (i >> 2);
-        const uint16_t *a = tile + t * BC + swizzle(t, c / 8) * 8 + c % 8;
+        const uint16_t *a = tile + t * kCols + swizzle(t, c / 8) * 8 + c % 8;
         u.h[p] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)a);
     }
     return u.v;
 }
 
-// BC x BC tiles of dW, 128 x 64 of them a wave (BC = 256) or 64 x 64
-template <int BC, int WK, int WN, bool kVec>
-__global__ __launch_bounds__((BC / WK) * (BC / WN) * kWave) void wgrad_kernel(const WgradArgs A) {
-    constexpr int kWavesK = BC / WK, kWaves = kWavesK * (BC / WN);
-    constexpr int FK = WK / 32, FN = WN / 32;
-    constexpr int kLoadRows = 512 / BC;                       // rows of a 1 KiB load
-    constexpr int kLoads = 2 * kRows / kLoadRows / kWaves;    // loads of a wave in a step
-    static_assert(2 * kRows % (kLoadRows * kWaves) == 0, "whole loads");
-    constexpr int kStage = 2 * kRows * BC;  // rows of x, then rows of dy
-    __shared__ __align__(16) uint16_t stages[2 * kStage];
+// The loads of one operand: a wave's 1 KiB loads hold whole LDS rows of kCols.
+template <int kCols, bool kVec>
+struct Operand {
+    static constexpr int kLoadRows = 512 / kCols;
+    static constexpr int kLoads = kRows / kLoadRows / kWaves;
+    const uint16_t *p[kLoads];  // this lane's 8 values of the next step
+    int64_t step;               // elements to the next step
+    int cols, col[kLoads];      // the matrix's columns, and each load's first
+
+    __device__ __forceinline__ static int row(int wave, int i) {
+        return (wave + i * kWaves) * kLoadRows + lane_id() / (kCols / 8);
+    }
+    __device__ __forceinline__ void set(const uint16_t *x, int64_t stride, int m, int c0, int width, int wave) {
+        step = stride * kRows;
+        cols = width;
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) {
+            const int r = row(wave, i);
+            col[i] = c0 + swizzle(r, lane_id() % (kCols / 8)) * 8;
+            p[i] = x + (int64_t)(m + r) * stride + col[i];
+        }
+    }
+    // load i into `tile`; rows: of the step that the group has
+    __device__ __forceinline__ void fetch(uint16_t *tile, int i, int rows, int wave) {
+        const bool in = row(wave, i) < rows && col[i] < cols;
+        uint16_t *to = tile + (wave + i * kWaves) * 512;
+        if constexpr (kVec) {
+            load_lds_1k(in ? static_cast<const void *>(p[i]) : static_cast<const void *>(kZeros), to);
+        } else {
+            u32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t a = in ? p[i][2 * j] : 0;
+                const uint32_t b = in && col[i] + 2 * j + 1 < cols ? p[i][2 * j + 1] : 0;
+                v[j] = a | (b << 16);
+            }
+            *reinterpret_cast<u32x4 *>(to + lane_id() * 8) = v;
+        }
+        p[i] += step;
+    }
+};
+
+template <bool kVec>
+__global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs A) {
+    constexpr int FK = kWaveK / 32, FN = kWaveN / 32;
+    constexpr int kStage = kRows * (kTileK + kTileN);  // rows of x, then rows of dy
+    typedef Operand<kTileK, kVec> X;
+    typedef Operand<kTileN, kVec> D;
+    constexpr int kLoads = X::kLoads + D::kLoads;
+    __shared__ __align__(16) uint16_t stages[kStages * kStage];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = lane_id();
-    const int tn = (A.N + BC - 1) / BC, tk = (A.K + BC - 1) / BC;
-    // an XCD takes consecutive tiles of one group
-    const int64_t all = (int64_t)A.groups.G * tn * tk, per = (all + 7) / 8;
-    const int64_t at = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
-    if (at >= all || blockIdx.x / 8 >= per) return;
-    const int g = (int)(at / ((int64_t)tn * tk)), in = (int)(at - (int64_t)g * tn * tk);
-    const int n0 = in / tk * BC, k0 = in % tk * BC;
+    const int tn = (A.N + kTileN - 1) / kTileN, tk = (A.K + kTileK - 1) / kTileK, tiles = (tn * tk + 7) / 8 * 8;
+    // Groups one after the other, so that a CU's two workgroups tend to come
+    // from different ones; in a group an XCD takes consecutive tiles.
+    const int g = blockIdx.x / tiles, at = blockIdx.x - g * tiles, in = at % 8 * (tiles / 8) + at / 8;
+    if (in >= tn * tk) return;
+    const int n0 = in / tk * kTileN, k0 = in % tk * kTileK;
     const int m0 = A.groups.start(g), m1 = A.groups.end(g);
     const int wk = wave % kWavesK, wn = wave / kWavesK;
 
@@ -89,71 +132,66 @@ __global__ __launch_bounds__((BC / WK) * (BC / WN) * kWave) void wgrad_kernel(co
 #pragma unroll
             for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
 
-    // this lane's chunk of each of the wave's loads: its row in the step and its
-    // columns; the first kRows rows of a stage are x, the others dy
-    auto fetch = [&](uint16_t *stage, int m) {
-#pragma unroll
-        for (int i = 0; i < kLoads; i++) {
-            const int r0 = (wave + i * kWaves) * kLoadRows;
-            const bool isx = r0 < kRows;
-            const int r = (r0 % kRows) + l / (BC / 8);
-            const int c = swizzle(r, l % (BC / 8)) * 8 + (isx ? k0 : n0), cols = isx ? A.K : A.N;
-            const uint16_t *p = isx ? A.x + (int64_t)(m + r) * A.x_stride : A.dy + (int64_t)(m + r) * A.dy_stride;
-            uint16_t *to = stage + r0 * BC;
-            if constexpr (kVec) {
-                const bool ok = m + r < m1 && c < cols;
-                load_lds_1k(ok ? static_cast<const void *>(p + c) : static_cast<const void *>(kZeros), to);
-            } else {
-                u32x4 v;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const uint32_t a = m + r < m1 && c + 2 * j < cols ? p[c + 2 * j] : 0;
-                    const uint32_t b = m + r < m1 && c + 2 * j + 1 < cols ? p[c + 2 * j + 1] : 0;
-                    v[j] = a | (b << 16);
-                }
-                *reinterpret_cast<u32x4 *>(to + l * 8) = v;
-            }
-        }
+    X x;
+    D d;
+    x.set(A.x, A.x_stride, m0, k0, A.K, wave);
+    d.set(A.dy, A.dy_stride, m0, n0, A.N, wave);
+    const int steps = (m1 - m0 + kRows - 1) / kRows;
+    // past the last step: zeros that nobody reads, so that the count of loads stays
+    auto fetch = [&](uint16_t *stage, int s, int i) {
+        const int rows = m1 - m0 - s * kRows;
+        if (i < X::kLoads) x.fetch(stage, i, rows, wave);
+        else d.fetch(stage + kRows * kTileK, i - X::kLoads, rows, wave);
     };
-    auto step = [&](const uint16_t *stage) {
-        const uint16_t *tx = stage, *td = stage + kRows * BC;
+    if (steps > 0) {
+#pragma unroll
+        for (int s = 0; s < kStages - 1; s++)
+#pragma unroll
+            for (int i = 0; i < kLoads; i++) fetch(stages + s * kStage, s, i);
+    }
+    int slot = 0;
+    for (int s = 0; s < steps; s++) {
+        // this step's stage is complete once every wave's loads are, and the
+        // stage before has been read
+        wait_loads_but<kVec ? (kStages - 2) * kLoads : 0>();
+        __syncthreads();
+        const uint16_t *tx = stages + slot * kStage, *td = tx + kRows * kTileK;
+        uint16_t *next = stages + (slot == 0 ? kStages - 1 : slot - 1) * kStage;
 #pragma unroll
         for (int t = 0; t < kRows; t += 16) {
             bf16x8 fx[FK], fd[FN];
 #pragma unroll
-            for (int i = 0; i < FK; i++) fx[i] = read_columns<BC>(tx, t, wk * WK + i * 32);
+            for (int i = 0; i < FK; i++) fx[i] = read_columns<kTileK>(tx, t, wk * kWaveK + i * 32);
 #pragma unroll
-            for (int j = 0; j < FN; j++) fd[j] = read_columns<BC>(td, t, wn * WN + j * 32);
+            for (int j = 0; j < FN; j++) fd[j] = read_columns<kTileN>(td, t, wn * kWaveN + j * 32);
 #pragma unroll
-            for (int i = 0; i < FK; i++)
+            for (int i = 0; i < FK; i++) {
 #pragma unroll
                 for (int j = 0; j < FN; j++)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[i], fd[j], acc[i][j], 0, 0, 0);
+                // the loads go out between the products, not all at the step's start
+                constexpr int kSlots = kRows / 16 * FK;
+#pragma unroll
+                for (int p = (t / 16 * FK + i) * kLoads / kSlots; p < (t / 16 * FK + i + 1) * kLoads / kSlots; p++)
+                    fetch(next, s + kStages - 1, p);
+            }
         }
-    };
-    if (m0 < m1) fetch(stages, m0);
-    for (int m = m0, b = 0; m < m1; m += kRows, b ^= 1) {
-        // this step's stage is complete once every wave's loads are, and the
-        // other stage has been read
-        wait_loads();
-        __syncthreads();
-        fetch(stages + (b ^ 1) * kStage, m + kRows);  // past the end: zeros that nobody reads
-        step(stages + b * kStage);
+        slot = slot == kStages - 1 ? 0 : slot + 1;
     }
-    wait_loads();
+    wait_loads();  // those that nobody reads
 
     int row;
     const bool spare = A.where.spare(g, &row);
     float *out = spare ? A.slot_out + row * A.slot_out_stride : A.out + row * A.out_stride;
 #pragma unroll
     for (int j = 0; j < FN; j++) {
-        const int n = n0 + wn * WN + j * 32 + (l & 31);
+        const int n = n0 + wn * kWaveN + j * 32 + (l & 31);
         if (n >= A.N) continue;
 #pragma unroll
         for (int i = 0; i < FK; i++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const int k = k0 + wk * WK + i * 32 + e * 8 + (l >> 5) * 4;
+                const int k = k0 + wk * kWaveK + i * 32 + e * 8 + (l >> 5) * 4;
                 float *o = out + (int64_t)n * A.K + k;
                 if (kVec && k + 4 <= A.K) {
                     *reinterpret_cast<f32x4 *>(o) = f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1],
@@ -167,13 +205,12 @@ __global__ __launch_bounds__((BC / WK) * (BC / WN) * kWave) void wgrad_kernel(co
     }
 }
 
-template <int BC, int WK, int WN>
 hipError_t launch(const WgradArgs &A, hipStream_t s) {
-    constexpr int kThreads = (BC / WK) * (BC / WN) * kWave;
-    const int64_t blocks = ceil_div((int64_t)A.groups.G * ceil_div(A.N, BC) * ceil_div(A.K, BC), 8) * 8;
+    const int64_t tiles = ceil_div(ceil_div(A.N, kTileN) * ceil_div(A.K, kTileK), 8) * 8;
+    const int64_t blocks = A.groups.G * tiles;
     if (blocks > 0xffffffffll / kThreads) return hipErrorInvalidConfiguration;
-    if (A.vec) wgrad_kernel<BC, WK, WN, true><<<(uint32_t)blocks, kThreads, 0, s>>>(A);
-    else wgrad_kernel<BC, WK, WN, false><<<(uint32_t)blocks, kThreads, 0, s>>>(A);
+    if (A.vec) wgrad_kernel<true><<<(uint32_t)blocks, kThreads, 0, s>>>(A);
+    else wgrad_kernel<false><<<(uint32_t)blocks, kThreads, 0, s>>>(A);
     return hipGetLastError();
 }
 
@@ -212,5 +249,5 @@ extern "C" int ep_grouped_wgrad(const ep_grouped_wgrad_t *p, ep_stream_t stream)
     A.vec = p->n % 8 == 0 && p->k % 8 == 0 && is_aligned(p->dy, 16) && is_aligned(p->x, 16) &&
             p->dy_stride % 8 == 0 && p->x_stride % 8 == 0 && is_aligned(p->out, 16) && p->out_stride % 4 == 0 &&
             is_aligned(p->slot_out, 16) && p->slot_out_stride % 4 == 0;
-    return rc_of(launch<256, 128, 64>(A, to_stream(stream)));
+    return rc_of(launch(A, to_stream(stream)));
 }
