@@ -14,6 +14,8 @@
 // maximum over the row choose instead.  The choice is the same either way.
 #pragma once
 
+#include <float.h>
+
 #include "layer.h"
 
 namespace ep {
@@ -47,9 +49,9 @@ struct GateSlot {
 // expert of register i of a lane
 __device__ __forceinline__ int gate_expert(int lane, int i) { return ((i / 8) * kGateLanes + lane) * 8 + i % 8; }
 
-// unsigned order of floats
+// unsigned order of floats, -0 and 0 alike
 __device__ __forceinline__ uint32_t float_order(float f) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, f);
+    const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
@@ -106,10 +108,7 @@ __device__ __forceinline__ void gate_scores(const GateArgs &A, int64_t t, int la
         }
     }
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        const float s = v[i] + 0.0f;  // -0 and 0 are equal scores
-        v[i] = s == s ? s : -INFINITY;
-    }
+    for (int i = 0; i < V; i++) v[i] = fmaxf(v[i], -INFINITY);  // the other operand where one is NaN
 }
 
 // Drops the scores outside the best groups.
@@ -212,44 +211,44 @@ __device__ __forceinline__ void gate_token(const GateArgs &A, int64_t t, GateSlo
 #pragma unroll
     for (int i = 1; i < V; i++) best = fmaxf(best, v[i]);
     // at least k lanes have fewer than k greater maxima, so k scores at least
-    // are not below the least of those maxima
-    const float tau = -row_max_f32(row_greater<1>(best) < A.k ? -best : -INFINITY);
-    int mine = 0;
+    // are not below the least of those maxima; -inf is no candidate
+    const float tau = fmaxf(-row_max_f32(row_greater<1>(best) < A.k ? -best : -INFINITY), -FLT_MAX);
+    uint64_t mine = 0;  // a bit for each candidate register
 #pragma unroll
-    for (int i = 0; i < V; i++) mine += v[i] >= tau && v[i] > -INFINITY;
-    const int upto = row_scan_i32(mine);
+    for (int i = 0; i < V; i++) mine |= v[i] >= tau ? 1ull << i : 0;
+    const int count = __popcll(mine);
+    const int upto = row_scan_i32(count);
     const int n = __shfl(upto, lane_id() | (kGateLanes - 1));
     if (__any(n > kGateCandidates)) {
         gate_rounds<V>(A, lane, slot, v);
     } else {
         slot->chosen[lane] = -1;
-        int at = upto - mine;
-#pragma unroll
-        for (int i = 0; i < V; i++)
-            if (v[i] >= tau && v[i] > -INFINITY) {
-                slot->score[at] = v[i];
-                slot->expert[at] = gate_expert(lane, i);
-                at++;
+        // a lane has few: the scores are formed again rather than picked out of
+        // the registers one by one
+        for (int at = upto - count; __any(mine != 0); at++) {
+            if (mine != 0) {
+                const int e = gate_expert(lane, __builtin_ctzll(mine));
+                slot->score[at] = gate_logit(A, t, e) + (A.bias ? A.bias[e] : 0.0f);
+                slot->expert[at] = e;
+                mine &= mine - 1;
             }
-        wave_lds_fence();
-        float s[2];
-        int e[2], before[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 2; c++) {
-            s[c] = slot->score[lane + c * kGateLanes];  // past the n-th: not used
-            e[c] = slot->expert[lane + c * kGateLanes];
         }
+        wave_lds_fence();
+        const bool two = __any(n > kGateLanes);
+        // past the n-th: not used
+        const float s0 = slot->score[lane], s1 = slot->score[lane + kGateLanes];
+        const int e0 = slot->expert[lane], e1 = slot->expert[lane + kGateLanes];
+        int before0 = 0, before1 = 0;
 #pragma unroll 4
         for (int o = 0; o < n; o++) {
             const float so = slot->score[o];
             const int eo = slot->expert[o];
-#pragma unroll
-            for (int c = 0; c < 2; c++) before[c] += so > s[c] || (so == s[c] && eo < e[c]);
+            before0 += so > s0 || (so == s0 && eo < e0);
+            if (two) before1 += so > s1 || (so == s1 && eo < e1);
         }
         wave_lds_fence();
-#pragma unroll
-        for (int c = 0; c < 2; c++)
-            if (lane + c * kGateLanes < n && before[c] < A.k) slot->chosen[before[c]] = e[c];
+        if (lane < n && before0 < A.k) slot->chosen[before0] = e0;
+        if (lane + kGateLanes < n && before1 < A.k) slot->chosen[before1] = e1;
     }
     wave_lds_fence();
     id = lane < A.k ? slot->chosen[lane] : -1;

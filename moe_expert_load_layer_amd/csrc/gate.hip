@@ -52,43 +52,45 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const GateArgs A, int64_
     }
 }
 
-// dl_j = w_j (g_j - sum_i w_i g_i / scale) at the chosen experts, 0 elsewhere
+// dl_j = w_j (g_j - sum_i w_i g_i / scale) at the chosen experts, 0 elsewhere.
+// A wave forms its 4 tokens' rows in LDS, in the output's type, and stores them
+// as one run of memory.
 template <bool kBf16>
 __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const int32_t *__restrict__ ids,
                                                                  const float *__restrict__ weights,
                                                                  const float *__restrict__ grad, int64_t T, int E,
                                                                  int k, float inv_scale, void *__restrict__ out) {
-    extern __shared__ float lds[];  // [kTokens][E]
-    const int s = threadIdx.x / kGateLanes, lane = threadIdx.x % kGateLanes;
-    const int64_t t0 = (int64_t)blockIdx.x * kTokens, t = t0 + s;
-    for (int i = threadIdx.x; i < kTokens * E; i += kThreads) lds[i] = 0.0f;
-    __syncthreads();
+    constexpr int kTok = kWave / kGateLanes, kWidth = kBf16 ? 2 : 4, kPer = 16 / kWidth;
+    extern __shared__ u32x4 lds[];  // [waves][4 rows of E, up to 16 bytes]
+    const int l = lane_id(), wave = threadIdx.x / kWave, lane = l % kGateLanes;
+    const int words = (kTok * E + kPer - 1) / kPer;  // of 16 bytes, a wave
+    u32x4 *mine = lds + wave * words;
+    const int64_t t0 = ((int64_t)blockIdx.x * (kThreads / kWave) + wave) * kTok, t = t0 + l / kGateLanes;
     const bool on = t < T && lane < k;
     const int id = on ? ids[t * k + lane] : -1;
     const bool use = id >= 0 && id < E;
     const float w = use ? weights[t * k + lane] : 0.0f;
     const float g = use ? grad[t * k + lane] : 0.0f;
+    for (int i = l; i < words; i += kWave) mine[i] = u32x4{0, 0, 0, 0};
     const float mean = row_sum_f32(w * g) * inv_scale;
-    if (use) lds[s * E + id] = w * (g - mean);
-    __syncthreads();
-    const int64_t n = min((int64_t)kTokens, T - t0) * E, o = t0 * E;
-    // the workgroup's rows are one run of memory; 16-byte stores, the end in single ones
-    constexpr int kPer = kBf16 ? 8 : 4;
-    const int64_t whole = (o % kPer == 0 && ((uintptr_t)out & 15) == 0) ? n / kPer : 0;
-    for (int64_t i = threadIdx.x; i < whole; i += kThreads) {
-        const float *p = lds + i * kPer;
-        if constexpr (kBf16) {
-            const u32x4 w4{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])};
-            reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(out) + o)[i] = w4;
-        } else {
-            reinterpret_cast<f32x4 *>(static_cast<float *>(out) + o)[i] = f32x4{p[0], p[1], p[2], p[3]};
-        }
+    wave_lds_fence();
+    if (use) {
+        const float d = w * (g - mean);
+        const int at = l / kGateLanes * E + id;
+        if constexpr (kBf16) reinterpret_cast<uint16_t *>(mine)[at] = to_bf16(d);
+        else reinterpret_cast<float *>(mine)[at] = d;
     }
-    for (int64_t i = whole * kPer + threadIdx.x; i < n; i += kThreads) {
+    wave_lds_fence();
+    if (t0 >= T) return;
+    const int64_t n = min((int64_t)kTok, T - t0) * E, o = t0 * E;  // o: a multiple of 4 elements
+    const int64_t whole = (o % kPer == 0 && ((uintptr_t)out & 15) == 0) ? n / kPer : 0;
+    u32x4 *to = reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(out) + o * kWidth);
+    for (int64_t i = l; i < whole; i += kWave) to[i] = mine[i];
+    for (int64_t i = whole * kPer + l; i < n; i += kWave) {
         if constexpr (kBf16)
-            static_cast<uint16_t *>(out)[o + i] = to_bf16(lds[i]);
+            static_cast<uint16_t *>(out)[o + i] = reinterpret_cast<const uint16_t *>(mine)[i];
         else
-            static_cast<float *>(out)[o + i] = lds[i];
+            static_cast<float *>(out)[o + i] = reinterpret_cast<const float *>(mine)[i];
     }
 }
 
@@ -128,7 +130,7 @@ extern "C" int ep_gate_topk_backward(const int32_t *ids, const float *weights, c
         return EP_ERR_INVALID_ARG;
     const float inv = gate->scale != 0.0f ? 1.0f / gate->scale : 0.0f;
     const dim3 grid((uint32_t)ceil_div(num_tokens, kTokens));
-    const size_t lds = (size_t)kTokens * gate->num_experts * sizeof(float);
+    const size_t lds = (size_t)(kThreads / kWave) * ceil_div(4 * (int64_t)gate->num_experts * (bf16 ? 2 : 4), 16) * 16;
     const hipStream_t s = to_stream(stream);
     if (bf16)
         gate_backward_kernel<true><<<grid, kThreads, lds, s>>>(ids, weights, grad_weights, num_tokens,

@@ -8,9 +8,11 @@ from __future__ import annotations
 import ctypes
 from typing import List, Optional, Sequence
 
+import numpy as np
 import torch
 
-from . import EPBalanceError, Layout, _arg, _check, _CLayout, _ptr, _stream, lib
+from . import EPBalanceError, Layout, _check, _CLayout, lib
+from . import _arg as _arg_or_raise
 
 EP_DTYPE_F32, EP_DTYPE_BF16, EP_DTYPE_FP8 = 0, 1, 2
 EP_MAX_FEW_TOKENS = 64
@@ -46,11 +48,6 @@ class _CExperts(ctypes.Structure):
                 ("down", _CMatrix)]
 
 
-class _CAdamWTensor(ctypes.Structure):
-    _fields_ = [("param", _vp), ("grad", _vp), ("exp_avg", _vp), ("exp_avg_sq", _vp), ("exp_avg_scale", _vp),
-                ("exp_avg_sq_scale", _vp), ("copy", _vp), ("numel", _i64)]
-
-
 class _CAdamW(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
@@ -82,8 +79,31 @@ def declare(L: ctypes.CDLL) -> None:
         getattr(L, f).restype = ctypes.c_int
 
 
+# These calls are a few microseconds of GPU time each in decoding, so that the checks and the stream's lookup take
+# the cheapest forms: one chain of comparisons where all is well, the messages only where it is not.
+
+def _arg(t: Optional[torch.Tensor], dtype: torch.dtype, shape, name: str) -> torch.Tensor:
+    """A contiguous device tensor of exactly this dtype and shape."""
+    if t is not None and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t
+    return _arg_or_raise(t, dtype, shape, name)
+
+
+def _ptr(t: torch.Tensor) -> int:
+    return t.data_ptr()
+
+
+def _stream(stream: Optional[torch.cuda.Stream]) -> int:
+    """The given stream, or torch's current one, as a pointer."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
+
+
 def _rows(t: torch.Tensor, dtypes, name: str) -> int:
     """A device matrix whose rows are contiguous; returns its row stride."""
+    if t.is_cuda and t.dtype in dtypes and t.dim() == 2:
+        (m, n), (sm, sn) = t.shape, t.stride()
+        if m > 1 and sm >= n and (sn == 1 or n <= 1):
+            return sm
     if not t.is_cuda:
         raise EPBalanceError(f"{name} must be a device tensor")
     if t.dtype not in dtypes:
@@ -146,7 +166,7 @@ def ep_gate_topk_backward(ids: torch.Tensor, weights: torch.Tensor, grad_weights
 
 def ep_scale_stride(cols: int) -> int:
     """Scale bytes of a row of `cols` values: its blocks of 128, up to a multiple of 4."""
-    return int(lib().ep_scale_stride(int(cols)))
+    return (cols + 511) // 512 * 4 if cols > 0 else 0
 
 
 def _up128(n: int) -> int:
@@ -389,39 +409,45 @@ class AdamW:
             self.exp_avg_scale, self.exp_avg_sq_scale = (
                 [torch.ones((p.numel() + 127) // 128, dtype=torch.uint8, device=p.device) for p in self.params]
                 for _ in range(2))
-        self._c = (_CAdamWTensor * max(1, len(self.params)))()
+        # the library's descriptors, one a row, as the 8 words of ep_adamw_tensor_t
+        self._words = np.zeros((len(self.params), 8), dtype=np.int64)
+        self._words[:, 7] = [p.numel() for p in self.params]
 
-    def _tensors(self):
-        """The descriptors; the lists above may have been given other tensors (a checkpoint's), so all are read."""
-        n = len(self.params)
-        lists = [(self.exp_avg, "exp_avg"), (self.exp_avg_sq, "exp_avg_sq")]
-        for name, what in (("exp_avg", self.exp_avg), ("exp_avg_sq", self.exp_avg_sq)):
-            if len(what) != n:
-                raise EPBalanceError(f"{name} must be one for each parameter")
+    def _tensors(self, grads: Optional[Sequence[torch.Tensor]] = None) -> int:
+        """The descriptors' address; the lists above may have been given other tensors (a checkpoint's), so all are
+        looked at."""
         state = torch.float32 if self.bits == 32 else torch.uint8
-        for i, (c, p) in enumerate(zip(self._c, self.params)):
-            c.param, c.numel = p.data_ptr(), p.numel()
-            for what, name in lists:
-                _arg(what[i], state, p.shape, f"{name}[{i}]")
-            c.exp_avg, c.exp_avg_sq = self.exp_avg[i].data_ptr(), self.exp_avg_sq[i].data_ptr()
-            if self.bits == 8:
-                blocks = ((p.numel() + 127) // 128,)
-                c.exp_avg_scale = _arg(self.exp_avg_scale[i], torch.uint8, blocks, "exp_avg_scale").data_ptr()
-                c.exp_avg_sq_scale = _arg(self.exp_avg_sq_scale[i], torch.uint8, blocks, "exp_avg_sq_scale").data_ptr()
-            c.copy = None if self.copies is None else self.copies[i].data_ptr()
-        return self._c
+        columns = [(0, self.params, torch.float32, "params"), (2, self.exp_avg, state, "exp_avg"),
+                   (3, self.exp_avg_sq, state, "exp_avg_sq")]
+        if grads is not None:
+            columns.append((1, grads, grads[0].dtype if grads else torch.float32, "grads"))
+        if self.copies is not None:
+            columns.append((6, self.copies, torch.bfloat16, "copies"))
+        shapes = [p.shape for p in self.params]
+        for word, tensors, dtype, name in columns:
+            if len(tensors) != len(shapes):
+                raise EPBalanceError(f"{name} must be one for each of the {len(shapes)} parameters")
+            for i, (t, shape) in enumerate(zip(tensors, shapes)):
+                if not (t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
+                    _arg_or_raise(t, dtype, shape, f"{name}[{i}]")
+            if shapes:
+                self._words[:, word] = [t.data_ptr() for t in tensors]
+        if self.bits == 8:
+            for word, tensors, name in ((4, self.exp_avg_scale, "exp_avg_scale"),
+                                        (5, self.exp_avg_sq_scale, "exp_avg_sq_scale")):
+                for i, (t, p) in enumerate(zip(tensors, self.params)):
+                    _arg(t, torch.uint8, ((p.numel() + 127) // 128,), f"{name}[{i}]")
+                if shapes:
+                    self._words[:, word] = [t.data_ptr() for t in tensors]
+        return self._words.ctypes.data
 
     def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, grad_scale: float = 1.0,
              stream=None) -> None:
         """One step; grads fp32 or bf16 (all the same), of the parameters' shapes."""
-        if len(grads) != len(self.params):
-            raise EPBalanceError(f"grads must be one for each of the {len(self.params)} parameters, got {len(grads)}")
         dtype = grads[0].dtype if grads else torch.float32
         if dtype not in _FLOATS:
             raise EPBalanceError(f"grads must be float32 or bfloat16, got {dtype}")
-        tensors = self._tensors()
-        for i, (g, p) in enumerate(zip(grads, self.params)):
-            tensors[i].grad = _arg(g, dtype, p.shape, f"grads[{i}]").data_ptr()
+        tensors = self._tensors(grads)
         hp = _CAdamW(self.lr if lr is None else lr, self.beta1, self.beta2, self.eps, self.weight_decay, grad_scale,
                      self.step_count + 1, self.seed, self.bits, _FLOATS[dtype])
         rc = lib().ep_adamw_step(tensors, len(self.params), ctypes.byref(hp), _stream(stream))
