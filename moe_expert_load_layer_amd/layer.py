@@ -11,7 +11,8 @@ from typing import List, Optional, Sequence
 import numpy as np
 import torch
 
-from . import EPBalanceError, Layout, _check, _CLayout, lib
+from . import (EPBalanceError, Layout, _check, _CLayout, ep_dispatch_layout, ep_load_histogram, ep_plan_quota,
+               ep_slot_fill, lib)
 from . import _arg as _arg_or_raise
 
 EP_DTYPE_F32, EP_DTYPE_BF16, EP_DTYPE_FP8 = 0, 1, 2
@@ -375,6 +376,57 @@ def ep_moe_few_tokens(x: torch.Tensor, logits: torch.Tensor, k: int, gate: torch
                                  _ptr(ids), _ptr(weights), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     _check(rc, "ep_moe_few_tokens")
     return out, ids, weights
+
+
+class ExpertRows:
+    """8-bit weights of a layer's experts, one packed row of bytes each: gate above up [2 I][H], down [H][I], then
+    their scales.  A row is what ep_slot_fill copies, so a buffer of spare slots has the same views."""
+
+    def __init__(self, count: int, hidden: int, inter: int, device):
+        self.hidden, self.inter = hidden, inter
+        hp, ip, hb, ib = _up128(hidden), _up128(inter), _up128(hidden) // 128, _up128(inter) // 128
+        nb = _up128(2 * inter) // 128
+        ends = np.cumsum([2 * inter * hp, hidden * ip, nb * hb, hb * ib])
+        self.rows = torch.zeros((count, int(-(-ends[3] // 16) * 16)), dtype=torch.uint8, device=device)
+        part = lambda a, b, n, k: self.rows[:, a:b].unflatten(1, (n, k))     # noqa: E731
+        self.gate_up = part(0, ends[0], 2 * inter, hp).view(_FP8)
+        self.down = part(ends[0], ends[1], hidden, ip).view(_FP8)
+        self.gate_up_scale, self.down_scale = part(ends[1], ends[2], nb, hb), part(ends[2], ends[3], hb, ib)
+
+    def load(self, gate_up: torch.Tensor, down: torch.Tensor) -> "ExpertRows":
+        """Rounds fp32 or bf16 matrices [E][2 I][H] and [E][H][I] into the rows."""
+        for w, q, s in ((gate_up, self.gate_up, self.gate_up_scale), (down, self.down, self.down_scale)):
+            wq, ws = ep_quant_blocks(w)
+            q.view(torch.uint8).copy_(wq.view(torch.uint8))
+            s.copy_(ws)
+        return self
+
+
+def run_layer(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layout, experts: ExpertRows, slots: ExpertRows,
+              bias=None, num_groups: int = 1, topk_groups: int = 1, scale: float = 1.0):
+    """One balanced mixture-of-experts layer over the tokens of all ranks, on the current stream: gate, load, plan,
+    replicas into the spare slots, dispatch order, the experts' products over the physical slots, combine.
+
+    x bf16 [tokens][H], logits [tokens][E] (rank by rank, the same number of tokens each); experts: the native
+    experts' rows, slots: the spare slots' (filled here).  Returns a dict: out bf16 [tokens][H], ids, weights, plan,
+    offsets, pos, src, h (the 8-bit input of the second product and its scales)."""
+    ids, weights = ep_gate_topk(logits, k, bias, num_groups, topk_groups, scale)
+    pairs = ids.view(1, -1)
+    load, ws, status = ep_load_histogram(pairs, layout)
+    plan = ep_plan_quota(load, layout, status=status)
+    offsets, pos, src = ep_dispatch_layout(pairs, layout, plan.phy_quota, plan.log2phy, plan.logcnt, ws)
+    if layout.num_spare:
+        ep_slot_fill(experts.rows, plan.phy2log[0], layout, slots.rows)
+    spare = (slots.gate_up, slots.gate_up_scale, slots.down, slots.down_scale) if layout.num_spare else (None,) * 4
+    xq, xs = ep_quant_rows(x)
+    up = ep_grouped_matmul(xq, xs, experts.gate_up, experts.gate_up_scale, offsets[0], rows=src[0], rows_div=k,
+                           layout=layout, slot_w=spare[0], slot_w_scale=spare[1])
+    h = ep_swiglu_quant(up)
+    y = ep_grouped_matmul(*h, experts.down, experts.down_scale, offsets[0], layout=layout, slot_w=spare[2],
+                          slot_w_scale=spare[3])
+    out = ep_moe_combine(y, pos.view(-1, k), weights)
+    return dict(out=out, ids=ids, weights=weights, plan=plan, status=status, offsets=offsets[0], pos=pos[0],
+                src=src[0], up=up, h=h, y=y)
 
 
 class AdamW:
