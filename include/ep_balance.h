@@ -465,9 +465,10 @@ typedef struct ep_matrix {
 
 /*
  * Grouped product: y[i] = w_g x[r(i)] for the output rows i of group g, the
- * consecutive rows offsets[g] .. offsets[g + 1] - 1.  Offsets outside [0, m] or
- * out of order are brought into range and order; rows from offsets[groups] on
- * become 0.
+ * consecutive rows offsets[g] .. offsets[g + 1] - 1, offsets[0] = 0.  Rows from
+ * offsets[groups] on become 0.  Offsets live on the device and cannot be refused:
+ * values outside [0, m] are brought into it and a group that ends before its start
+ * is empty, so that no access leaves a buffer.
  *   x, x_scale  as ep_quant_rows writes them: k columns, x_rows rows
  *   rows        device int32 [m] or NULL: r(i) = rows[i] / rows_div (the pair
  *               that a dispatch position serves, rows_div = top-k); a negative
@@ -478,7 +479,7 @@ typedef struct ep_matrix {
  *               holds the native experts [E] and slot_w the spare slots [S]
  *               (the slot buffer), and slot_offsets of ep_dispatch_layout are
  *               the offsets
- *   y           device bf16 [m][n], every element written
+ *   y           device bf16 [m][n], every element written (with such offsets)
  * The input gradient is the same call on the quantised output gradient with
  * weights from ep_quant_blocks(transpose = 1).  m < 2^31 - 1024.
  */

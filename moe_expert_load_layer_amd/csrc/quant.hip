@@ -5,6 +5,12 @@
 // largest magnitude is at most 448 scales.  Scaling by a power of two is exact,
 // so a value is rounded once, to nearest with ties to even.  NaN and infinities
 // become NaN.  All four kernels are one pass over the data, bound by HBM.
+// Measured, bytes read and written once (a 2 GiB copy reaches 4.95 TB/s):
+//   rows of bf16      65536 x 4096      147 us  5.5 TB/s   (8192 x 4096: 24 us, 4.2)
+//   rows of fp32      32768 x 4096      114 us  5.9 TB/s
+//   silu(g) u         65536 x 2 x 2048  125 us  5.4 TB/s
+//   blocks of bf16    16 x 8192 x 4096  288 us  5.6 TB/s, transposed or not
+//   combine           8192 x 8 x 4096   126 us  4.8 TB/s
 //
 // A unit is one row's block: 16 lanes (a DPP row) of 8 values, so that loads
 // are 16 (bf16) or 32 bytes a lane and the block's maximum takes 4 DPP steps.
@@ -95,7 +101,10 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const void *__rest
     if (lane == 0) scale[m * sb + b] = (uint8_t)c;
 }
 
-// the same for silu(gate) * up, gate and up the halves of a bf16 row of 2 I values
+// The same for silu(gate) * up, gate and up the halves of a bf16 row of 2 I
+// values.  The sigmoid takes the hardware's exponential and reciprocal (2^-16 of
+// a value at most, against the 2^-4 of the rounding that follows): with exact
+// division and exponential, arithmetic bounds the pass, 199 us for 65536 x 2048.
 __global__ __launch_bounds__(kThreads) void swiglu_quant_kernel(const uint16_t *__restrict__ x, int64_t M, int64_t I,
                                                                 int kb, int sb, bool vec, uint8_t *__restrict__ q,
                                                                 uint8_t *__restrict__ scale) {
@@ -112,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_quant_kernel(const uint16_t *
     load_row8<true>(x, m * 2 * I, (int64_t)b * kScaleBlock + lane * 8, I, vec, g);
     load_row8<true>(x, m * 2 * I + I, (int64_t)b * kScaleBlock + lane * 8, I, vec, v);
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] *= g[j] / (1.0f + expf(-g[j]));
+    for (int j = 0; j < 8; j++) v[j] *= g[j] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[j]));
     const int c = fp8_scale_code(row_max_f32(amax8(v)));
     *reinterpret_cast<u32x2 *>(q + (m * kb + b) * kScaleBlock + lane * 8) = to_fp8(v, c);
     if (lane == 0) scale[m * sb + b] = (uint8_t)c;

@@ -7,10 +7,16 @@
 //
 // The sum runs over the rows of both operands, so both tiles are needed
 // transposed: rows go into LDS as they lie in memory (without passing
-// registers, two stages deep, one barrier a step), and ds_read_b64_tr hands
-// each lane 4 consecutive rows of one column.  It reads 4 rows of 32 bytes for
-// 16 lanes; the 16-byte chunks of an LDS row are exchanged by the row's bits
-// 0, 1 and 3, so that the rows read together meet different banks.
+// registers, a ring of three stages of 32 rows, one barrier a step), and
+// ds_read_b64_tr hands each lane 4 consecutive rows of one column.  It reads 4
+// rows of 32 bytes for 16 lanes; the 16-byte chunks of an LDS row are exchanged
+// by the row's bits 0 and 1, so that the rows read together meet different banks.
+//
+// Bound: the matrix pipes.  16381 rows in 3 groups, N = 2048, K = 4096: 326 us,
+// 840 TFLOP/s, against 1190 of a large library product in bf16.  Tiles of
+// 256 x 128 by 4 waves of 128 x 64 leave LDS for two workgroups a CU: while one
+// waits at its barrier or stores its tile, the other multiplies.  One workgroup
+// of 256 x 256 a CU takes 339 us.
 //
 // x is the instruction's row operand: a lane ends with 4 consecutive k of one n
 // and stores 16 bytes.  Rows past the group's end and columns past the matrix
