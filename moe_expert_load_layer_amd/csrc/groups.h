@@ -40,25 +40,21 @@ struct GroupRows {
 bool layout_groups(const ep_layout_t *layout, int32_t groups, bool slots, GroupRows *where);
 
 // The tile-th tile of T rows over the groups in order, found by every wave for
-// itself: *g its group, *first its tiles before.  Group G stands for the rows
-// past the last offset.  Returns false past the last tile.  *total: all tiles.
+// itself: *g its group, *first the tiles before that group.  Returns false past
+// the last tile; total_tiles is their number.
 __device__ __forceinline__ int group_tiles(const Groups &R, int g, int T) {
-    if (g > R.G) return 0;
-    int rows;
-    if (g < R.G) rows = R.end(g) - R.start(g);
-    else rows = R.offsets ? R.M - R.start(R.G) : 0;
-    return (rows + T - 1) / T;
+    return g < R.G ? (R.end(g) - R.start(g) + T - 1) / T : 0;
 }
 
 __device__ __forceinline__ int total_tiles(const Groups &R, int T) {
     int total = 0;
-    for (int g0 = 0; g0 <= R.G; g0 += kWave) total += wave_sum_i32(group_tiles(R, g0 + lane_id(), T));
+    for (int g0 = 0; g0 < R.G; g0 += kWave) total += wave_sum_i32(group_tiles(R, g0 + lane_id(), T));
     return total;
 }
 
 __device__ __forceinline__ bool find_tile(const Groups &R, int T, int tile, int *g, int *first) {
     int before = 0;
-    for (int g0 = 0; g0 <= R.G; g0 += kWave) {
+    for (int g0 = 0; g0 < R.G; g0 += kWave) {
         const int c = group_tiles(R, g0 + lane_id(), T);
         const int incl = wave_incl_scan_i32(c);
         const int sum = __builtin_amdgcn_readlane(incl, kWave - 1);
@@ -78,13 +74,22 @@ __device__ __forceinline__ bool find_tile(const Groups &R, int T, int tile, int 
 // `lds` + 16 i, `lds` the same in every lane.  It has no register result and
 // is counted in vmcnt; wait_loads() waits for this wave's.  Written in asm
 // because the compiler would wait for every such load before any later read
-// of LDS, also of the other stage.
+// of LDS, also of the other stage.  The forms below take 4 bytes a lane, or one
+// byte that gets 4 in LDS: lane i's at `lds` + 4 i.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is named as changed on purpose
-__device__ __forceinline__ void load_lds_1k(const void *g, void *lds) {
-    const uint32_t base = __builtin_amdgcn_readfirstlane(
-        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds);
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(base), "v"(g) : "m0", "memory");
+__device__ __forceinline__ uint32_t lds_address(void *lds) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds);
+}
+__device__ __forceinline__ void load_lds_1k(const void *g, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "m0", "memory");
+}
+__device__ __forceinline__ void load_lds_1k(const void *g, void *lds) { load_lds_1k(g, lds_address(lds)); }
+__device__ __forceinline__ void load_lds_dwords(const void *g, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(g) : "m0", "memory");
+}
+__device__ __forceinline__ void load_lds_bytes(const void *g, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(g) : "m0", "memory");
 }
 #pragma clang diagnostic pop
 

@@ -20,9 +20,10 @@
 // read LDS, then all multiply.  So a step's operands are read into registers
 // during the step before, each right after the products that free its
 // registers, and the loads into LDS go out between the products too (issued
-// together they wait for the address unit: 8 % slower).  At 65536 x 4096 x 4096
-// the matrix pipes are busy 57 % of the cycles, at 1.8 GHz (the card lowers its
-// clock from 2.4 under this load): 2.0 PFLOP/s alone, 1.9 in a row.
+// together they wait for the address unit: 8 % slower).  At 65536 x 4096 x 4096:
+// 976 us, 2.25 PFLOP/s, against 2.93 of a large library product in 8 bits without
+// scales; zeros instead of random values take a fifth less, as the card lowers
+// its clock (2.4 GHz to 1.8) under this load.
 #include "groups.h"
 
 namespace ep {
@@ -49,10 +50,17 @@ struct MatmulArgs {
 // rows (256 bytes, a cycle's worth) meet every bank once.
 constexpr int kStep = 64;
 constexpr int kParts = kScaleBlock / kStep;
-constexpr int kScaleBlocks = 32;             // blocks of a chunk of scales; two chunks are in LDS
-constexpr int kScaleRow = kScaleBlocks + 4;  // rows 9 banks apart
+constexpr int kScaleBlocks = 32;  // blocks of a chunk of scales; three chunks are in LDS
+constexpr int kWScaleBytes = 256;  // of a chunk: 32 scales of each 128 rows of w (two at most), 4 bytes each
 
 __device__ __forceinline__ int exchange(int row, int chunk) { return chunk ^ ((row >> 2) & 3); }
+
+// A chunk of x scales is 32 bytes a row, their dwords exchanged by the row's bits
+// 3 and 4: 32 rows' scales of one block lie in 32 banks.
+__device__ __forceinline__ int scale_exchange(int row) { return (row >> 3 & 3) << 2; }
+__device__ __forceinline__ int scale_at(int row, int block) {
+    return (row * kScaleBlocks | scale_exchange(row)) ^ block;
+}
 
 // this lane's 32 bytes of LDS row r (lanes 0 .. 31 the first half of its 64)
 __device__ __forceinline__ i32x8 read_frag(const uint8_t *tile, int r) {
@@ -74,13 +82,12 @@ __device__ __forceinline__ i32x8 read_frag(const uint8_t *tile, int r) {
 // statements hold the products in this order: together at the front, they would
 // leave nothing to wait behind.
 template <int BM, int FM, int FN, int kLoads, int kWaves>
-__device__ __forceinline__ void matmul_step(const uint8_t *next, uint8_t *fill, const uint8_t *(&src)[kLoads],
-                                            int ahead, int wave, int xrow, int wrow, const uint8_t *xs,
-                                            const uint8_t *ws, const i32x8 (&fx)[FM], i32x8 (&nx)[FM],
-                                            i32x8 (&fw)[FN], const int (&sx)[FM], int (&ns)[FM], int &sw,
-                                            f32x16 (&acc)[FN][FM]) {
+__device__ __forceinline__ void matmul_step(const uint8_t *next, uint32_t fill, const uint8_t *(&src)[kLoads],
+                                            int ahead, int xrow, int wrow, const uint8_t *xs, const uint8_t *ws,
+                                            int block, const i32x8 (&fx)[FM], i32x8 (&nx)[FM], i32x8 (&fw)[FN],
+                                            const int (&sx)[FM], int (&ns)[FM], int &sw, f32x16 (&acc)[FN][FM]) {
     const int r = lane_id() & 31;
-    const int nsw = ws[0];
+    const int nsw = ws[block * 4];
 #pragma unroll
     for (int i = 0; i < FN; i++) {
         asm volatile("" : "+v"(fw[i]));
@@ -91,20 +98,27 @@ __device__ __forceinline__ void matmul_step(const uint8_t *next, uint8_t *fill, 
 #pragma unroll
             for (int j = 0; j < FM; j++) {
                 nx[j] = read_frag(next, xrow + j * 32 + r);
-                ns[j] = xs[(xrow + j * 32 + r) * kScaleRow];
+                ns[j] = xs[scale_at(xrow + r, block) + j * 32 * kScaleBlocks];
             }
         }
         fw[i] = read_frag(next, BM + wrow + i * 32 + r);
 #pragma unroll
         for (int p = i * kLoads / FN; p < (i + 1) * kLoads / FN; p++) {
-            load_lds_1k(src[p], fill + (wave + p * kWaves) * 1024);
+            load_lds_1k(src[p], fill + p * kWaves * 1024);
             src[p] += ahead;
+            asm volatile("" : "+v"(src[p]));  // one pointer a load, not one for each of two steps
         }
     }
     sw = nsw;
 }
 
-// kStages: the next step's stage, the one being filled, and those in flight
+// A workgroup takes one tile after the other, and the ring never empties: a
+// tile's last steps fetch the first ones of the next.  Finding a tile, its rows'
+// places, the first loads and the wait for them, and the stores of the tile
+// before cost 12 us a tile where each of them had a workgroup of its own.
+//
+// kStages: the next step's stage, those in flight, and this step's, whose
+// operands are in registers and which is filled again.
 template <int BM, int BN, int WM, int WN, int kStages>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kernel(const MatmulArgs A) {
     constexpr int kWavesM = BM / WM, kWaves = kWavesM * (BN / WN), kThreads = kWaves * kWave;
@@ -112,174 +126,261 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
     constexpr int kLoadRows = 1024 / kStep;
     constexpr int kLoads = (BM + BN) / kLoadRows / kWaves;  // 1 KiB loads of a wave in a step
     constexpr int kStage = (BM + BN) * kStep;
-    constexpr int kWScales = (BN + kScaleBlock - 1) / kScaleBlock, kChunk = (BM + kWScales) * kScaleRow;
+    constexpr int kChunk = BM * kScaleBlocks + kWScaleBytes;  // bytes of a chunk of scales: of x, then of w
+    constexpr int kScaleLoads = BM * (kScaleBlocks / 4) / kThreads;
+    constexpr int kStores = FM * FN * 2;  // 16-byte stores of a lane for a full tile
     static_assert((BM + BN) % (kLoadRows * kWaves) == 0 && BM % kLoadRows == 0, "whole loads");
-    static_assert(kScaleBlock % WN == 0, "a wave's columns share a scale");
+    static_assert(BM * (kScaleBlocks / 4) % kThreads == 0 && BM <= kThreads, "whole loads of scales");
+    static_assert(kScaleBlock % WN == 0 && BN <= 2 * kScaleBlock, "a wave's columns share a scale");
+    static_assert(kStages % 2 == 0 && (kStages - 2) * kLoads + kStores < 64, "steps go in pairs; a wait's largest count");
     __shared__ __align__(16) uint8_t stages[kStages * kStage];
-    __shared__ __align__(16) uint8_t scales[2 * kChunk];
+    __shared__ __align__(16) uint8_t scales[3 * kChunk];
+    // This tile and the next one, in LDS rather than in registers: a tile's rows and
+    // columns, its matrix, and the row of x of each of its rows (-1: none)
+    struct Tile {
+        int m0, m1, n0;
+        const uint8_t *w, *ws;
+    };
+    __shared__ Tile tiles[2];
+    __shared__ int32_t places[2][BM];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = lane_id();
+    const int wm = wave % kWavesM, wn = wave / kWavesM;
     const int nt = (A.N + BN - 1) / BN;
-    const int mt = total_tiles(A.groups, BM);
+    const int mt = __builtin_amdgcn_readfirstlane(total_tiles(A.groups, BM));  // kept in a scalar register
     // the workgroups of one XCD (consecutive ones go round the 8 XCDs) take
     // consecutive tiles: 4 row tiles by all column tiles, columns last, so that
     // the tiles in flight on an XCD share rows of x and of w in its L2
-    const int64_t all = (int64_t)mt * nt;
-    const int64_t per = (all + 7) / 8;
-    const int64_t at = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
-    if (blockIdx.x / 8 >= per || at >= all) return;
-    constexpr int kBand = 4;
-    const int band = (int)(at / ((int64_t)kBand * nt));
-    const int in = (int)(at - (int64_t)band * kBand * nt), high = min(kBand, mt - band * kBand);
-    const int tn = in / high, tile = band * kBand + in % high;
-    int g, first;
-    if (!find_tile(A.groups, BM, tile, &g, &first)) return;
-    const bool tail = g == A.groups.G;  // rows past the last group: zeros
-    const int m0 = A.groups.start(g) + (tile - first) * BM;
-    const int m1 = tail ? A.groups.M : A.groups.end(g);
-    const int n0 = tn * BN;
+    const int64_t all = (int64_t)mt * nt, per = (all + 7) / 8;
+    const int64_t from = blockIdx.x % 8 * per, to = min(from + per, all);
+    const int stride = gridDim.x / 8;
+    const int64_t row_bytes = (int64_t)A.kb * 128;
+    const int steps = A.kb * kParts;  // even
+    const bool vec = A.N % 8 == 0 && ((uintptr_t)A.y & 15) == 0;
 
-    const int wm = wave % kWavesM, wn = wave / kWavesM;
-    f32x16 acc[FN][FM];
-#pragma unroll
-    for (int i = 0; i < FN; i++)
-#pragma unroll
-        for (int j = 0; j < FM; j++)
-#pragma unroll
-            for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
-
-    // x row of output row m, -1: none
-    auto source = [&](int m) {
-        if (!A.rows) return m;
-        const int p = A.rows[m];
-        const int r = p < 0 ? -1 : p / A.rows_div;
-        return r < A.x_rows ? r : -1;
+    // What is computed once a tile from the lane's number starts from this copy, or
+    // its values would be kept in registers throughout.
+    auto lane_now = [] {
+        int v = lane_id();
+        asm volatile("" : "+v"(v));
+        return v;
     };
-
-    if (!tail) {
+    // finds the at-th tile and puts it into tiles[buf] and places[buf]
+    auto locate = [&](int64_t at, int buf) {
+        const int thread = wave * kWave + lane_now();
+        constexpr int kBand = 4;
+        const int band = (int)(at / ((int64_t)kBand * nt));
+        const int in = (int)(at - (int64_t)band * kBand * nt), high = min(kBand, mt - band * kBand);
+        const int tn = in / high, tile = band * kBand + in % high;
+        int g = 0, first = 0;
+        find_tile(A.groups, BM, tile, &g, &first);
+        Tile t;
+        t.m0 = A.groups.start(g) + (tile - first) * BM;
+        t.m1 = A.groups.end(g);
+        t.n0 = tn * BN;
         int row;
         const bool spare = A.where.spare(g, &row);
-        const uint8_t *w = spare ? A.slot_w + row * A.slot_w_stride : A.w + row * A.w_stride;
-        const uint8_t *ws = spare ? A.slot_ws + row * A.slot_ws_stride : A.ws + row * A.ws_stride;
-        const int64_t row_bytes = (int64_t)A.kb * 128;
-
-        // the 16 bytes that this lane fetches in each of the wave's loads
-        const uint8_t *src[kLoads];
+        t.w = spare ? A.slot_w + row * A.slot_w_stride : A.w + row * A.w_stride;
+        t.ws = spare ? A.slot_ws + row * A.slot_ws_stride : A.ws + row * A.ws_stride;
+        if (thread == 0) tiles[buf] = t;
+        if (thread < BM) {
+            int r = min(t.m0 + thread, t.m1 - 1);  // rows past the end repeat the last
+            if (A.rows) {
+                const int p = A.rows[r];
+                r = p < 0 ? -1 : p / A.rows_div;
+                r = r < A.x_rows ? r : -1;
+            }
+            places[buf][thread] = r;
+        }
+        __syncthreads();
+    };
+    // the 16 bytes that this lane fetches in each of the wave's loads of step 0
+    const uint8_t *src[kLoads];
+    auto sources = [&](int buf) {
+        const Tile &t = tiles[buf];
+        const int l = lane_now();
 #pragma unroll
         for (int i = 0; i < kLoads; i++) {
             const int r = (wave + i * kWaves) * kLoadRows + l / (kStep / 16), c = exchange(r, l % (kStep / 16));
-            if (r < BM) {
-                const int s = source(min(m0 + r, m1 - 1));  // rows past the end repeat the last
-                src[i] = A.x + max(s, 0) * row_bytes + c * 16;
-            } else {
-                src[i] = w + (int64_t)min(n0 + r - BM, A.N - 1) * row_bytes + c * 16;
-            }
+            if (r < BM) src[i] = A.x + max(places[buf][r], 0) * row_bytes + c * 16;
+            else src[i] = t.w + (int64_t)min(t.n0 + r - BM, A.N - 1) * row_bytes + c * 16;
         }
-        // scale bytes of blocks b0 .. b0 + 31: 4 blocks of a row a thread
-        auto scale_bytes = [&](int b0) {
-            uint8_t *to = scales + (b0 / kScaleBlocks & 1) * kChunk;
-            const int nb = min(kScaleBlocks, A.kb - b0);
-            for (int i = threadIdx.x; i < BM * (kScaleBlocks / 4); i += kThreads) {
-                const int r = i / (kScaleBlocks / 4), b = i % (kScaleBlocks / 4) * 4;
-                if (b < nb) {
-                    const int s = source(min(m0 + r, m1 - 1));
-                    *reinterpret_cast<uint32_t *>(to + r * kScaleRow + b) =
-                        *reinterpret_cast<const uint32_t *>(A.xs + (int64_t)max(s, 0) * A.sb + b0 + b);
-                }
-            }
-            for (int i = threadIdx.x; i < kWScales * kScaleBlocks; i += kThreads) {
-                const int j = i / kScaleBlocks, b = i % kScaleBlocks;
-                if (b < nb)
-                    to[(BM + j) * kScaleRow + b] =
-                        ws[(int64_t)min(n0 / kScaleBlock + j, (A.N - 1) / kScaleBlock) * A.kb + b0 + b];
-            }
-        };
-        const int steps = A.kb * kParts;  // even
+    };
+    // starts the loads of scale chunk `chunk` of a tile
+    auto scale_loads = [&](int buf, int chunk, int slot) {
+        const Tile &t = tiles[buf];
+        const uint32_t to = lds_address(scales) + slot * kChunk;
+        const int l = lane_now();
+        const int b0 = chunk * kScaleBlocks;
 #pragma unroll
-        for (int p = 0; p < kStages - 1; p++)
+        for (int i = 0; i < kScaleLoads; i++) {
+            const int r = (wave + i * kWaves) * 8 + l / 8;
+            // dwords past the row's end repeat its last one and are not used
+            const int at = min(b0 + (l % 8 * 4 ^ scale_exchange(r)), A.sb - 4);
+            load_lds_dwords(A.xs + (int64_t)max(places[buf][r], 0) * A.sb + at, to + (wave + i * kWaves) * 256);
+        }
+        const int nb = min(t.n0 / kScaleBlock + l / kScaleBlocks, (A.N - 1) / kScaleBlock);
+        // every wave the same bytes to the same place
+        load_lds_bytes(t.ws + (int64_t)nb * A.kb + min(b0 + l % kScaleBlocks, A.kb - 1), to + BM * kScaleBlocks);
+    };
+
+    int64_t at = from + blockIdx.x / 8;
+    if (at < to) {
+        const uint32_t ring = lds_address(stages) + wave * 1024;
+        int buf = 0, slot = 0, chunk0 = 0;  // chunk0: where the tile's first chunk of scales lies
+        locate(at, buf);
+        sources(buf);
+        scale_loads(buf, 0, chunk0);
+#pragma unroll
+        for (int p = 0; p < kStages; p++)
 #pragma unroll
             for (int i = 0; i < kLoads; i++) {
                 load_lds_1k(src[i], stages + p * kStage + (wave + i * kWaves) * 1024);
                 src[i] += p + 1 < steps ? kStep : 0;
             }
-        scale_bytes(0);
-        if (A.kb > kScaleBlocks) scale_bytes(kScaleBlocks);
-        wait_loads_but<(kStages - 2) * kLoads>();
+        wait_loads_but<(kStages - 1) * kLoads>();
         __syncthreads();
+        f32x16 acc[FN][FM];
         i32x8 fx[FM], fx2[FM], fw[FN];
-        int sx[FM], sx2[FM], sw = scales[(BM + wn * WN / kScaleBlock) * kScaleRow];
+        int sx[FM], sx2[FM], sw = scales[BM * kScaleBlocks + wn * WN / kScaleBlock * kScaleBlocks * 4];
 #pragma unroll
         for (int j = 0; j < FM; j++) {
             fx[j] = read_frag(stages, wm * WM + j * 32 + (l & 31));
-            sx[j] = scales[(wm * WM + j * 32 + (l & 31)) * kScaleRow];
+            sx[j] = scales[scale_at(wm * WM + (l & 31), 0) + j * 32 * kScaleBlocks];
         }
 #pragma unroll
         for (int i = 0; i < FN; i++) fw[i] = read_frag(stages, BM + wn * WN + i * 32 + (l & 31));
-        int slot = 0;
-        // step s: its operands are in `fx`, `sx` and fw, the next one's go to `nx`, `ns`
-        auto step = [&](int s, const i32x8 (&x)[FM], i32x8 (&nx)[FM], const int (&c)[FM], int (&nc)[FM]) {
-            // the next step's stage is complete once every wave's loads are, and
-            // the stage to fill has been read
-            wait_loads_but<(kStages - 3) * kLoads>();
-            __syncthreads();
-            const int after = (slot + 1) % kStages, b = (s + 1) / kParts;
-            const uint8_t *xs = scales + (b / kScaleBlocks & 1) * kChunk + b % kScaleBlocks;
-            matmul_step<BM, FM, FN, kLoads, kWaves>(stages + after * kStage, stages + (slot + kStages - 1) % kStages * kStage,
-                                                    src, s + kStages < steps ? kStep : 0, wave, wm * WM, wn * WN, xs,
-                                                    xs + (BM + wn * WN / kScaleBlock) * kScaleRow, x, nx, fw, c, nc, sw,
-                                                    acc);
-            slot = after;
-        };
-        for (int b0 = 0; b0 < A.kb; b0 += kScaleBlocks) {
-            const int s1 = kParts * min(b0 + kScaleBlocks, A.kb);
-            for (int s = kParts * b0; s < s1; s += 2) {
-                step(s, fx, fx2, sx, sx2);
-                step(s + 1, fx2, fx, sx2, sx);
+        for (;;) {
+#pragma unroll
+            for (int i = 0; i < FN; i++)
+#pragma unroll
+                for (int j = 0; j < FM; j++)
+#pragma unroll
+                    for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+            const bool more = at + stride < to;
+            const int chunks = (A.kb + kScaleBlocks - 1) / kScaleBlocks;
+            int ahead = kStep;
+            // A step: its operands are in x, c and fw, the next one's (block `block` of
+            // the chunk at `chunk`) go to nx, nc and fw.
+            auto step = [&](int chunk, int block, const i32x8 (&x)[FM], i32x8 (&nx)[FM], const int (&c)[FM],
+                            int (&nc)[FM]) {
+                // the next step's stage is complete once every wave's loads are, and
+                // this step's has been read by all
+                wait_loads_but<(kStages - 2) * kLoads>();
+                __syncthreads();
+                const int after = slot == kStages - 1 ? 0 : slot + 1;
+                const uint8_t *xs = scales + chunk;
+                matmul_step<BM, FM, FN, kLoads, kWaves>(
+                    stages + after * kStage, ring + slot * kStage, src, ahead, wm * WM, wn * WN, xs,
+                    xs + BM * kScaleBlocks + wn * WN / kScaleBlock * kScaleBlocks * 4, block, x, nx, fw, c, nc, sw, acc);
+                slot = after;
+            };
+            // Between the steps at which something happens besides, the loop is bare.
+            for (int s = 0; s < steps;) {
+                if (s % (kParts * kScaleBlocks) == 0) {
+                    const int ch = s / (kParts * kScaleBlocks) + 1;
+                    if (ch < chunks) scale_loads(buf, ch, (chunk0 + ch) % 3);
+                }
+                if (more && s == steps - kStages - 4) {
+                    locate(at + stride, buf ^ 1);
+                    scale_loads(buf ^ 1, 0, (chunk0 + chunks) % 3);
+                }
+                if (s == max(steps - kStages, 0)) {  // from here on steps of the next tile are fetched
+                    if (more) {
+                        sources(buf ^ 1);
+                    } else {  // or bytes that nobody reads, so that the count of loads stays
+                        ahead = 0;
+#pragma unroll
+                        for (int i = 0; i < kLoads; i++) src[i] = tiles[buf].w;
+                    }
+                }
+                // the chunk's last step, and with it the next chunk's place
+                const int ch = s / (kParts * kScaleBlocks), end = min(steps, (ch + 1) * (kParts * kScaleBlocks));
+                const int here = (chunk0 + ch) % 3 * kChunk, there = (chunk0 + ch + 1) % 3 * kChunk;
+                int stop = end;
+                if (s < steps - kStages) stop = min(stop, steps - kStages);
+                if (more && s < steps - kStages - 4) stop = min(stop, steps - kStages - 4);
+                for (int b = s / kParts % kScaleBlocks; s < stop; s += 2, b++) {
+                    step(here, b, fx, fx2, sx, sx2);  // the second half of this block
+                    const bool last = s + 2 == end;
+                    step(last ? there : here, last ? 0 : b + 1, fx2, fx, sx2, sx);
+                }
             }
-            if (b0 + 2 * kScaleBlocks < A.kb) {
-                __syncthreads();  // this chunk's scales have been read
-                scale_bytes(b0 + 2 * kScaleBlocks);
-            }
-        }
-        wait_loads();  // those that nobody reads
-    }
 
-    // Two lanes exchange halves of their rows of 4 values, for 16-byte stores.
-    const bool vec = A.N % 8 == 0 && ((uintptr_t)A.y & 15) == 0;
-#pragma unroll
-    for (int j = 0; j < FM; j++) {
-        const int m = m0 + wm * WM + j * 32 + (l & 31);
-        const bool in = m < m1, real = in && !tail && source(m) >= 0;
-        uint16_t *y = A.y + (int64_t)m * A.N;
-#pragma unroll
-        for (int i = 0; i < FN; i++)
-#pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-                const f32x16 &c = acc[i][j];
+            // Two lanes exchange halves of their rows of 4 values, for 16-byte stores.
+            const int l = lane_now();
+            const Tile &tile = tiles[buf];
+            const bool full =
+                __builtin_amdgcn_readfirstlane(vec && tile.m0 + BM <= tile.m1 && tile.n0 + BN <= A.N);
+            auto eight = [&](const f32x16 &c, int e, bool real) {
                 const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(c[e], c[e + 1]), pack_bf16(c[e + 4], c[e + 5]),
                                                                 false, false);
                 const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(c[e + 2], c[e + 3]),
                                                                 pack_bf16(c[e + 6], c[e + 7]), false, false);
-                u32x4 v{a[0], b[0], a[1], b[1]};  // n .. n + 7
-                if (!real) v = u32x4{0, 0, 0, 0};
-                const int n = n0 + wn * WN + i * 32 + e * 2 + (l >> 5) * 8;
-                if (vec) {
-                    if (in && n < A.N) *reinterpret_cast<u32x4 *>(y + n) = v;
-                } else if (in) {
+                return real ? u32x4{a[0], b[0], a[1], b[1]} : u32x4{0, 0, 0, 0};  // n .. n + 7
+            };
 #pragma unroll
-                    for (int q = 0; q < 8; q++)
-                        if (n + q < A.N) y[n + q] = (uint16_t)(v[q / 2] >> (16 * (q % 2)));
+            for (int j = 0; j < FM; j++) {
+                const int r = wm * WM + j * 32 + (l & 31), m = tile.m0 + r, n0 = tile.n0 + wn * WN + (l >> 5) * 8;
+                const bool real = places[buf][r] >= 0;
+                uint16_t *y = A.y + (int64_t)m * A.N + n0;
+                if (full) {
+#pragma unroll
+                    for (int i = 0; i < FN; i++)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8)
+                            *reinterpret_cast<u32x4 *>(y + i * 32 + e * 2) = eight(acc[i][j], e, real);
+                } else {
+                    const int end = m < tile.m1 ? A.N - n0 : 0;
+#pragma unroll
+                    for (int i = 0; i < FN; i++)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8) {
+                            const u32x4 v = eight(acc[i][j], e, real);
+                            const int n = i * 32 + e * 2;
+                            if (vec) {
+                                if (n < end) *reinterpret_cast<u32x4 *>(y + n) = v;
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < 8; q++)
+                                    if (n + q < end) y[n + q] = (uint16_t)(v[q / 2] >> (16 * (q % 2)));
+                            }
+                        }
                 }
             }
+            if (!more) break;
+            at += stride;
+            buf ^= 1;
+            chunk0 = (chunk0 + chunks) % 3;
+        }
+        wait_loads();  // those that nobody reads
+    }
+
+    // rows past the last group: zeros
+    if (!A.groups.offsets) return;
+    const int64_t z0 = (int64_t)A.groups.start(A.groups.G) * A.N, z1 = (int64_t)A.groups.M * A.N;
+    const int64_t threads = (int64_t)gridDim.x * kThreads, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (vec) {
+        for (int64_t i = z0 + id * 8; i < z1; i += threads * 8) *reinterpret_cast<u32x4 *>(A.y + i) = u32x4{0, 0, 0, 0};
+    } else {
+        for (int64_t i = z0 + id; i < z1; i += threads) A.y[i] = 0;
     }
 }
 
 template <int BM, int BN, int WM, int WN, int kStages>
 hipError_t launch(const MatmulArgs &A, hipStream_t s) {
     constexpr int kThreads = (BM / WM) * (BN / WN) * kWave;
-    // every group may end in a part tile, and so may the rows past the last
-    const int64_t mt = A.groups.M / BM + A.groups.G + 1;
-    const int64_t blocks = ceil_div(mt * ceil_div(A.N, BN), 8) * 8;
+    // every group may end in a part tile
+    const int64_t mt = A.groups.M / BM + A.groups.G;
+    int64_t blocks = ceil_div(mt * ceil_div(A.N, BN), 8) * 8;
+    // As many workgroups as the card holds; each its own tile where a tile's steps
+    // are too few: the next tile is found kStages + 4 steps before the end, and not
+    // before a barrier after the last tile's stores.
+    const void *kernel = (const void *)matmul_kernel<BM, BN, WM, WN, kStages>;
+    if (A.kb * kParts > kStages + 4) {
+        const int64_t resident = resident_blocks(kernel, kThreads, 0) / 8 * 8;
+        if (resident > 0 && resident < blocks) blocks = resident;
+    }
     if (blocks > 0xffffffffll / kThreads) return hipErrorInvalidConfiguration;
     matmul_kernel<BM, BN, WM, WN, kStages><<<(uint32_t)blocks, kThreads, 0, s>>>(A);
     return hipGetLastError();
