@@ -39,11 +39,12 @@ struct GateArgs {
 constexpr int kGateCandidates = 2 * kGateLanes;
 
 // LDS of one token
-struct GateSlot {
+struct alignas(16) GateSlot {
+    uint64_t key[kGateCandidates];  // of a candidate: its score's order, then ~expert; 0: none
+    float logit[kGateCandidates];
     int32_t chosen[kGateMaxK];
+    float chosen_logit[kGateMaxK];
     uint32_t group[kGateMaxGroups];
-    float score[kGateCandidates];
-    int32_t expert[kGateCandidates];
 };
 
 // expert of register i of a lane
@@ -107,8 +108,6 @@ __device__ __forceinline__ void gate_scores(const GateArgs &A, int64_t t, int la
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < V; i++) v[i] = fmaxf(v[i], -INFINITY);  // the other operand where one is NaN
 }
 
 // Drops the scores outside the best groups.
@@ -207,52 +206,78 @@ __device__ __forceinline__ void gate_token(const GateArgs &A, int64_t t, GateSlo
     float v[V];
     gate_scores<V>(A, t, lane, v);
     if (A.G > 1) gate_groups<V>(A, lane, slot, v);
-    float best = v[0];
+    float best = -INFINITY;  // fmaxf takes the other operand where one is NaN
 #pragma unroll
-    for (int i = 1; i < V; i++) best = fmaxf(best, v[i]);
+    for (int i = 0; i < V; i++) best = fmaxf(best, v[i]);
     // at least k lanes have fewer than k greater maxima, so k scores at least
     // are not below the least of those maxima; -inf is no candidate
     const float tau = fmaxf(-row_max_f32(row_greater<1>(best) < A.k ? -best : -INFINITY), -FLT_MAX);
-    uint64_t mine = 0;  // a bit for each candidate register
+    constexpr int kWords = (V + 31) / 32;
+    uint32_t mine[kWords];  // a bit for each candidate register
+    int count = 0;
 #pragma unroll
-    for (int i = 0; i < V; i++) mine |= v[i] >= tau ? 1ull << i : 0;
-    const int count = __popcll(mine);
+    for (int h = 0; h < kWords; h++) {
+        mine[h] = 0;
+#pragma unroll
+        for (int i = min(V, 32 * h + 32) - 1; i >= 32 * h; i--) mine[h] += mine[h] + (v[i] >= tau ? 1u : 0u);
+        count += __popc(mine[h]);
+    }
     const int upto = row_scan_i32(count);
     const int n = __shfl(upto, lane_id() | (kGateLanes - 1));
+    float l;
     if (__any(n > kGateCandidates)) {
         gate_rounds<V>(A, lane, slot, v);
+        wave_lds_fence();
+        id = lane < A.k ? slot->chosen[lane] : -1;
+        l = id >= 0 ? gate_logit(A, t, id) : -INFINITY;
     } else {
         slot->chosen[lane] = -1;
+        slot->key[lane] = slot->key[lane + kGateLanes] = 0;
+        wave_lds_fence();
         // a lane has few: the scores are formed again rather than picked out of
         // the registers one by one
-        for (int at = upto - count; __any(mine != 0); at++) {
-            if (mine != 0) {
-                const int e = gate_expert(lane, __builtin_ctzll(mine));
-                slot->score[at] = gate_logit(A, t, e) + (A.bias ? A.bias[e] : 0.0f);
-                slot->expert[at] = e;
-                mine &= mine - 1;
+        int at = upto - count;
+#pragma unroll
+        for (int h = 0; h < kWords; h++)
+            for (; __any(mine[h] != 0); at++) {
+                if (mine[h] == 0) {
+                    at--;
+                } else {
+                    const int e = gate_expert(lane, 32 * h + __builtin_ctz(mine[h]));
+                    const float raw = gate_logit(A, t, e);
+                    slot->key[at] = (uint64_t)float_order(raw + (A.bias ? A.bias[e] : 0.0f)) << 32 | (uint32_t)~e;
+                    slot->logit[at] = raw;
+                    mine[h] &= mine[h] - 1;
+                }
             }
-        }
         wave_lds_fence();
         const bool two = __any(n > kGateLanes);
-        // past the n-th: not used
-        const float s0 = slot->score[lane], s1 = slot->score[lane + kGateLanes];
-        const int e0 = slot->expert[lane], e1 = slot->expert[lane + kGateLanes];
+        const uint64_t k0 = slot->key[lane], k1 = slot->key[lane + kGateLanes];
+        const float l0 = slot->logit[lane], l1 = slot->logit[lane + kGateLanes];  // past the n-th: not used
         int before0 = 0, before1 = 0;
-#pragma unroll 4
-        for (int o = 0; o < n; o++) {
-            const float so = slot->score[o];
-            const int eo = slot->expert[o];
-            before0 += so > s0 || (so == s0 && eo < e0);
-            if (two) before1 += so > s1 || (so == s1 && eo < e1);
+        for (int o = 0; o < n; o += 4) {
+            uint64_t key[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) key[i] = slot->key[o + i];
+#pragma unroll
+            for (int i = 0; i < 4; i++) before0 += key[i] > k0;
+            if (two) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) before1 += key[i] > k1;
+            }
+        }
+        if (lane < n && before0 < A.k) {
+            slot->chosen[before0] = (int32_t)~(uint32_t)k0;
+            slot->chosen_logit[before0] = l0;
+        }
+        if (lane + kGateLanes < n && before1 < A.k) {
+            slot->chosen[before1] = (int32_t)~(uint32_t)k1;
+            slot->chosen_logit[before1] = l1;
         }
         wave_lds_fence();
-        if (lane < n && before0 < A.k) slot->chosen[before0] = e0;
-        if (lane + kGateLanes < n && before1 < A.k) slot->chosen[before1] = e1;
+        id = lane < A.k ? slot->chosen[lane] : -1;
+        l = id >= 0 ? slot->chosen_logit[lane] : -INFINITY;
     }
-    wave_lds_fence();
-    id = lane < A.k ? slot->chosen[lane] : -1;
-    const float l = id >= 0 ? gate_logit(A, t, id) : -INFINITY;
     const float top = row_max_f32(l);
     // l == top also where both are infinite
     const float e = id < 0 ? 0.0f : (l == top ? 1.0f : expf(l - top));
