@@ -12,11 +12,11 @@
 // rows of 32 bytes for 16 lanes; the 16-byte chunks of an LDS row are exchanged
 // by the row's bits 0 and 1, so that the rows read together meet different banks.
 //
-// Bound: the matrix pipes.  16381 rows in 3 groups, N = 2048, K = 4096: 326 us,
-// 840 TFLOP/s, against 1190 of a large library product in bf16.  Tiles of
+// Bound: the matrix pipes.  16381 rows in 3 groups, N = 2048, K = 4096: 316 us,
+// 870 TFLOP/s, against 1190 of a large library product in bf16.  Tiles of
 // 256 x 128 by 4 waves of 128 x 64 leave LDS for two workgroups a CU: while one
 // waits at its barrier or stores its tile, the other multiplies.  One workgroup
-// of 256 x 256 a CU takes 339 us.
+// of 256 x 256 a CU took 13 us more.
 //
 // x is the instruction's row operand: a lane ends with 4 consecutive k of one n
 // and stores 16 bytes.  Rows past the group's end and columns past the matrix
@@ -41,6 +41,7 @@ struct WgradArgs {
     float *out, *slot_out;
     int64_t out_stride, slot_out_stride;  // elements between groups
     bool vec;                             // 16-byte rows and stores
+    int32_t band;                         // tiles of x side by side, see the kernel
 };
 
 constexpr int kRows = 32;              // rows of a step
@@ -123,10 +124,13 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs A) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = lane_id();
     const int tn = (A.N + kTileN - 1) / kTileN, tk = (A.K + kTileK - 1) / kTileK, tiles = (tn * tk + 7) / 8 * 8;
     // Groups one after the other, so that a CU's two workgroups tend to come
-    // from different ones; in a group an XCD takes consecutive tiles.
+    // from different ones.  In a group an XCD takes consecutive tiles, counted along
+    // bands of x, so that its L2 serves about as many columns of x as of dy (0.54 GB
+    // from memory for 16381 rows, 2048 x 4096; with all of x in one band 1.14 GB).
     const int g = blockIdx.x / tiles, at = blockIdx.x - g * tiles, in = at % 8 * (tiles / 8) + at / 8;
     if (in >= tn * tk) return;
-    const int n0 = in / tk * kTileN, k0 = in % tk * kTileK;
+    const int bar = in / (A.band * tn), rest = in - bar * A.band * tn, wide = min(A.band, tk - bar * A.band);
+    const int n0 = rest / wide * kTileN, k0 = (bar * A.band + rest % wide) * kTileK;
     const int m0 = A.groups.start(g), m1 = A.groups.end(g);
     const int wk = wave % kWavesK, wn = wave / kWavesK;
 
@@ -211,8 +215,11 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs A) {
     }
 }
 
-hipError_t launch(const WgradArgs &A, hipStream_t s) {
+hipError_t launch(WgradArgs &A, hipStream_t s) {
     const int64_t tiles = ceil_div(ceil_div(A.N, kTileN) * ceil_div(A.K, kTileK), 8) * 8;
+    // an XCD's eighth of the tiles, as a rectangle of about as many columns of x as of dy
+    A.band = 1;
+    while ((int64_t)(A.band + 1) * (A.band + 1) * (kTileK / kTileN) <= tiles / 8) A.band++;
     const int64_t blocks = A.groups.G * tiles;
     if (blocks > 0xffffffffll / kThreads) return hipErrorInvalidConfiguration;
     if (A.vec) wgrad_kernel<true><<<(uint32_t)blocks, kThreads, 0, s>>>(A);
