@@ -79,3 +79,19 @@ def test_many_tiles(dev, M, N, K, G, spread, gather):
     y.fill_(3.0)
     ep.ep_grouped_matmul(xq, xs, wq, ws, off, rows=r, rows_div=2 if gather else 1, y=y)
     assert torch.equal(y, first)
+
+
+@pytest.mark.parametrize("N,K,sizes", [(1160, 2568, (170, 0, 130)), (2048, 4096, (64, 33)), (3000, 1031, (200,))])
+def test_wgrad_many_tiles(dev, N, K, sizes):
+    # exact products of bf16, fp32 additions: (m + 8) 2^-24 of the sum of magnitudes
+    M = sum(sizes)
+    g = torch.Generator(device=dev).manual_seed(N)
+    dy = torch.randn((M, N), generator=g, device=dev).to(torch.bfloat16)
+    x = torch.randn((M, K), generator=g, device=dev).to(torch.bfloat16)
+    ends = np.concatenate([[0], np.cumsum(sizes)])
+    off = torch.tensor(ends, dtype=torch.int32, device=dev)
+    got = ep.ep_grouped_wgrad(dy, x, off, out=torch.full((len(sizes), N, K), 7.0, device=dev))
+    for e, m in enumerate(sizes):
+        i, j = int(ends[e]), int(ends[e + 1])
+        a, b = dy[i:j].double().T.contiguous(), x[i:j].double()
+        assert ((got[e].double() - a @ b).abs() <= (m + 8) * 2.0 ** -24 * (a.abs() @ b.abs())).all(), e
