@@ -40,7 +40,6 @@ constexpr int kMLow = 896, kVLow = 768;                    // pattern >> 20 of c
 struct Args {
     ep_adamw_tensor_t t[kMaxTensors];
     uint32_t first[kMaxTensors + 1];  // first workgroup of each tensor
-    uint8_t vec[kMaxTensors];         // all of its arrays are 16-byte aligned
     int32_t n;
 };
 
@@ -96,19 +95,19 @@ __device__ __forceinline__ int find_tensor(const Args &A, uint32_t b) {
 
 // 8 values from `base + i`; past the end zeros
 template <typename T, bool kBf16>
-__device__ __forceinline__ void load8(const void *base, int64_t i, int left, bool vec, float (&x)[kUnit]) {
+__device__ __forceinline__ void load8(const void *base, int64_t i, int left, float (&x)[kUnit]) {
     const T *p = static_cast<const T *>(base) + i;
-    if (vec && left >= kUnit) {
+    if (left >= kUnit) {
         if constexpr (kBf16) {
-            const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+            const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_at2 *>(p));
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 x[2 * k] = bf16_lo(w[k]);
                 x[2 * k + 1] = bf16_hi(w[k]);
             }
         } else {
-            const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p));
-            const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p) + 1);
+            const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_at4 *>(p));
+            const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_at4 *>(p) + 1);
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 x[k] = a[k];
@@ -126,11 +125,11 @@ __device__ __forceinline__ void load8(const void *base, int64_t i, int left, boo
     }
 }
 
-__device__ __forceinline__ void store8(float *base, int64_t i, int left, bool vec, const float (&x)[kUnit]) {
+__device__ __forceinline__ void store8(float *base, int64_t i, int left, const float (&x)[kUnit]) {
     float *p = base + i;
-    if (vec && left >= kUnit) {
-        __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(p));
-        __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4 *>(p) + 1);
+    if (left >= kUnit) {
+        __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4_at4 *>(p));
+        __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4_at4 *>(p) + 1);
     } else {
 #pragma unroll
         for (int k = 0; k < kUnit; k++)
@@ -138,10 +137,10 @@ __device__ __forceinline__ void store8(float *base, int64_t i, int left, bool ve
     }
 }
 
-__device__ __forceinline__ void load_codes(const void *base, int64_t i, int left, bool vec, uint32_t (&q)[kUnit]) {
+__device__ __forceinline__ void load_codes(const void *base, int64_t i, int left, uint32_t (&q)[kUnit]) {
     const uint8_t *p = static_cast<const uint8_t *>(base) + i;
-    if (vec && left >= kUnit) {
-        const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+    if (left >= kUnit) {
+        const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_at1 *>(p));
 #pragma unroll
         for (int k = 0; k < kUnit; k++) q[k] = (w[k / 4] >> (8 * (k % 4))) & 255u;
     } else {
@@ -150,13 +149,13 @@ __device__ __forceinline__ void load_codes(const void *base, int64_t i, int left
     }
 }
 
-__device__ __forceinline__ void store_codes(void *base, int64_t i, int left, bool vec, const uint32_t (&q)[kUnit]) {
+__device__ __forceinline__ void store_codes(void *base, int64_t i, int left, const uint32_t (&q)[kUnit]) {
     uint8_t *p = static_cast<uint8_t *>(base) + i;
-    if (vec && left >= kUnit) {
+    if (left >= kUnit) {
         u32x2 w;
         w[0] = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
         w[1] = q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24);
-        __builtin_nontemporal_store(w, reinterpret_cast<u32x2 *>(p));
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x2_at1 *>(p));
     } else {
 #pragma unroll
         for (int k = 0; k < kUnit; k++)
@@ -169,20 +168,19 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args A, const Hyp
 #pragma clang fp contract(off)
     const int ti = find_tensor(A, blockIdx.x);
     const ep_adamw_tensor_t &t = A.t[ti];
-    const bool vec = A.vec[ti];
     const int64_t i = (int64_t)(blockIdx.x - A.first[ti]) * kChunk + (int64_t)threadIdx.x * kUnit;
     const int left = (int)min((int64_t)kUnit, t.numel - i);  // may be negative: the lane stores nothing
     float p[kUnit], g[kUnit], m[kUnit], v[kUnit];
-    load8<float, false>(t.param, i, left, vec, p);
+    load8<float, false>(t.param, i, left, p);
     if constexpr (kGradBf16)
-        load8<uint16_t, true>(t.grad, i, left, vec, g);
+        load8<uint16_t, true>(t.grad, i, left, g);
     else
-        load8<float, false>(t.grad, i, left, vec, g);
+        load8<float, false>(t.grad, i, left, g);
     const int64_t block = i / kScaleBlock;
     if constexpr (kEight) {
         uint32_t qm[kUnit], qv[kUnit];
-        load_codes(t.exp_avg, i, left, vec, qm);
-        load_codes(t.exp_avg_sq, i, left, vec, qv);
+        load_codes(t.exp_avg, i, left, qm);
+        load_codes(t.exp_avg_sq, i, left, qv);
         const float sm = pow2_of(left > 0 ? t.exp_avg_scale[block] : 1);
         const float sv = pow2_of(left > 0 ? t.exp_avg_sq_scale[block] : 1);
 #pragma unroll
@@ -191,8 +189,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args A, const Hyp
             v[k] = decode_v(qv[k], sv);
         }
     } else {
-        load8<float, false>(t.exp_avg, i, left, vec, m);
-        load8<float, false>(t.exp_avg_sq, i, left, vec, v);
+        load8<float, false>(t.exp_avg, i, left, m);
+        load8<float, false>(t.exp_avg_sq, i, left, v);
     }
 #pragma unroll
     for (int k = 0; k < kUnit; k++) {
@@ -201,14 +199,14 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args A, const Hyp
         v[k] = v[k] * H.beta2 + (x * x) * H.rest2;
         p[k] = p[k] * H.decay - H.rate * (m[k] / (sqrtf(v[k]) * H.root + H.eps));
     }
-    store8(t.param, i, left, vec, p);
+    store8(t.param, i, left, p);
     if (t.copy) {
         uint16_t *c = static_cast<uint16_t *>(t.copy) + i;
-        if (vec && left >= kUnit) {
+        if (left >= kUnit) {
             u32x4 w;
 #pragma unroll
             for (int k = 0; k < 4; k++) w[k] = pack_bf16(p[2 * k], p[2 * k + 1]);
-            __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(c));
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x4_at2 *>(c));
         } else {
 #pragma unroll
             for (int k = 0; k < kUnit; k++)
@@ -232,15 +230,15 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args A, const Hyp
             qv[k] = encode_v(v[k], iv, h & 0xfffffu);
             qm[k] = encode_m(m[k], im, (h * 0x9E3779B9u) >> 12);
         }
-        store_codes(t.exp_avg, i, left, vec, qm);
-        store_codes(t.exp_avg_sq, i, left, vec, qv);
+        store_codes(t.exp_avg, i, left, qm);
+        store_codes(t.exp_avg_sq, i, left, qv);
         if (threadIdx.x % (kScaleBlock / kUnit) == 0 && left > 0) {
             t.exp_avg_scale[block] = (uint8_t)cm;
             t.exp_avg_sq_scale[block] = (uint8_t)cv;
         }
     } else {
-        store8(static_cast<float *>(t.exp_avg), i, left, vec, m);
-        store8(static_cast<float *>(t.exp_avg_sq), i, left, vec, v);
+        store8(static_cast<float *>(t.exp_avg), i, left, m);
+        store8(static_cast<float *>(t.exp_avg_sq), i, left, v);
     }
 }
 
@@ -249,13 +247,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args A, const Hyp
 __global__ __launch_bounds__(kThreads) void adamw_values_kernel(const Args A) {
     const int ti = find_tensor(A, blockIdx.x);
     const ep_adamw_tensor_t &t = A.t[ti];
-    const bool vec = A.vec[ti];
     const int64_t i = (int64_t)(blockIdx.x - A.first[ti]) * kChunk + (int64_t)threadIdx.x * kUnit;
     const int left = (int)min((int64_t)kUnit, t.numel - i);
     if (left <= 0) return;
     uint32_t qm[kUnit], qv[kUnit];
-    load_codes(t.exp_avg, i, left, vec, qm);
-    load_codes(t.exp_avg_sq, i, left, vec, qv);
+    load_codes(t.exp_avg, i, left, qm);
+    load_codes(t.exp_avg_sq, i, left, qv);
     const float sm = pow2_of(t.exp_avg_scale[i / kScaleBlock]), sv = pow2_of(t.exp_avg_sq_scale[i / kScaleBlock]);
     float m[kUnit], v[kUnit];
 #pragma unroll
@@ -263,8 +260,8 @@ __global__ __launch_bounds__(kThreads) void adamw_values_kernel(const Args A) {
         m[k] = decode_m(qm[k], sm);
         v[k] = decode_v(qv[k], sv);
     }
-    store8(t.param, i, left, vec, m);
-    store8(static_cast<float *>(t.copy), i, left, vec, v);
+    store8(t.param, i, left, m);
+    store8(static_cast<float *>(t.copy), i, left, v);
 }
 
 // Calls launch(args, workgroups, index of the first tensor) for as many
@@ -282,8 +279,6 @@ int for_batches(const ep_adamw_tensor_t *tensors, int32_t n, F launch) {
             const ep_adamw_tensor_t &t = tensors[i];
             A.t[A.n] = t;
             A.first[A.n] = (uint32_t)blocks;
-            A.vec[A.n] = is_aligned(t.param, 16) && is_aligned(t.grad, 16) && is_aligned(t.exp_avg, 16) &&
-                         is_aligned(t.exp_avg_sq, 16) && is_aligned(t.copy, 16);
             A.n++;
             blocks += b;
         }

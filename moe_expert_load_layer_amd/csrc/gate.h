@@ -32,8 +32,6 @@ struct GateArgs {
     int32_t E, k, G, TG;
     float scale;
     int32_t bf16;  // the logits' type
-    int32_t vec;   // rows start on 16 bytes
-    int32_t bias_vec;
 };
 
 constexpr int kGateCandidates = 2 * kGateLanes;
@@ -67,17 +65,18 @@ __device__ __forceinline__ void gate_scores(const GateArgs &A, int64_t t, int la
 #pragma unroll
     for (int i = 0; i < V; i += 8) {
         const int e = gate_expert(lane, i);
-        if (A.vec && e + 8 <= A.E) {
+        if (e + 8 <= A.E) {
             if (A.bf16) {
-                const u32x4 w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(A.logits) +
-                                                                 t * A.stride + e);
+                const u32x4 w = *reinterpret_cast<const u32x4_at2 *>(static_cast<const uint16_t *>(A.logits) +
+                                                                     t * A.stride + e);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     v[i + 2 * j] = bf16_lo(w[j]);
                     v[i + 2 * j + 1] = bf16_hi(w[j]);
                 }
             } else {
-                const f32x4 *p = reinterpret_cast<const f32x4 *>(static_cast<const float *>(A.logits) + t * A.stride + e);
+                const f32x4_at4 *p =
+                    reinterpret_cast<const f32x4_at4 *>(static_cast<const float *>(A.logits) + t * A.stride + e);
                 const f32x4 a = p[0], b = p[1];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
@@ -94,8 +93,8 @@ __device__ __forceinline__ void gate_scores(const GateArgs &A, int64_t t, int la
 #pragma unroll
         for (int i = 0; i < V; i += 8) {
             const int e = gate_expert(lane, i);
-            if (A.bias_vec && e + 8 <= A.E) {
-                const f32x4 *p = reinterpret_cast<const f32x4 *>(A.bias + e);
+            if (e + 8 <= A.E) {
+                const f32x4_at4 *p = reinterpret_cast<const f32x4_at4 *>(A.bias + e);
                 const f32x4 a = p[0], b = p[1];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {

@@ -21,7 +21,6 @@ bool gate_ok(const ep_gate_t *g) {
 
 GateArgs gate_args(const void *logits, int64_t stride, const ep_gate_t *g) {
     GateArgs A;
-    const int width = g->logits_dtype == EP_DTYPE_BF16 ? 2 : 4;
     A.logits = logits;
     A.stride = stride;
     A.bias = g->bias;
@@ -31,8 +30,6 @@ GateArgs gate_args(const void *logits, int64_t stride, const ep_gate_t *g) {
     A.TG = g->topk_groups;
     A.scale = g->scale;
     A.bf16 = g->logits_dtype == EP_DTYPE_BF16;
-    A.vec = is_aligned(logits, 16) && (stride * width) % 16 == 0;
-    A.bias_vec = is_aligned(g->bias, 16);
     return A;
 }
 
@@ -86,9 +83,8 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const int32_t *
     }
     wave_lds_fence();
     if (t0 >= T) return;
-    const int64_t n = min((int64_t)kTok, T - t0) * E, o = t0 * E;  // o: a multiple of 4 elements
-    const int64_t whole = (o % kPer == 0 && ((uintptr_t)out & 15) == 0) ? n / kPer : 0;
-    u32x4 *to = reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(out) + o * kWidth);
+    const int64_t n = min((int64_t)kTok, T - t0) * E, o = t0 * E, whole = n / kPer;
+    u32x4_at2 *to = reinterpret_cast<u32x4_at2 *>(static_cast<uint8_t *>(out) + o * kWidth);
     for (int64_t i = l; i < whole; i += kWave) to[i] = mine[i];
     for (int64_t i = whole * kPer + l; i < n; i += kWave) {
         if constexpr (kBf16)

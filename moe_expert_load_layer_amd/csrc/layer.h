@@ -9,6 +9,11 @@ namespace ep {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// Vectors in memory at any address that their elements may have: the card takes
+// them in one access, so rows of odd lengths cost no more instructions.
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_at1 __attribute__((aligned(1)));
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kScaleBlock = 128;  // values that share one scale byte

@@ -156,7 +156,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
     const int stride = gridDim.x / 8;
     const int64_t row_bytes = (int64_t)A.kb * 128;
     const int steps = A.kb * kParts;  // even
-    const bool vec = A.N % 8 == 0 && ((uintptr_t)A.y & 15) == 0;
 
     // What is computed once a tile from the lane's number starts from this copy, or
     // its values would be kept in registers throughout.
@@ -311,7 +310,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
             const int l = lane_now();
             const Tile &tile = tiles[buf];
             const bool full =
-                __builtin_amdgcn_readfirstlane(vec && tile.m0 + BM <= tile.m1 && tile.n0 + BN <= A.N);
+                __builtin_amdgcn_readfirstlane(tile.m0 + BM <= tile.m1 && tile.n0 + BN <= A.N);
             auto eight = [&](const f32x16 &c, int e, bool real) {
                 const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(c[e], c[e + 1]), pack_bf16(c[e + 4], c[e + 5]),
                                                                 false, false);
@@ -329,7 +328,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
                     for (int i = 0; i < FN; i++)
 #pragma unroll
                         for (int e = 0; e < 16; e += 8)
-                            *reinterpret_cast<u32x4 *>(y + i * 32 + e * 2) = eight(acc[i][j], e, real);
+                            *reinterpret_cast<u32x4_at2 *>(y + i * 32 + e * 2) = eight(acc[i][j], e, real);
                 } else {
                     const int end = m < tile.m1 ? A.N - n0 : 0;
 #pragma unroll
@@ -338,8 +337,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
                         for (int e = 0; e < 16; e += 8) {
                             const u32x4 v = eight(acc[i][j], e, real);
                             const int n = i * 32 + e * 2;
-                            if (vec) {
-                                if (n < end) *reinterpret_cast<u32x4 *>(y + n) = v;
+                            if (n + 8 <= end) {
+                                *reinterpret_cast<u32x4_at2 *>(y + n) = v;
                             } else {
 #pragma unroll
                                 for (int q = 0; q < 8; q++)
@@ -360,10 +359,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
     if (!A.groups.offsets) return;
     const int64_t z0 = (int64_t)A.groups.start(A.groups.G) * A.N, z1 = (int64_t)A.groups.M * A.N;
     const int64_t threads = (int64_t)gridDim.x * kThreads, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (vec) {
-        for (int64_t i = z0 + id * 8; i < z1; i += threads * 8) *reinterpret_cast<u32x4 *>(A.y + i) = u32x4{0, 0, 0, 0};
-    } else {
-        for (int64_t i = z0 + id; i < z1; i += threads) A.y[i] = 0;
+    for (int64_t i = z0 + id * 8; i < z1; i += threads * 8) {
+        if (i + 8 <= z1) *reinterpret_cast<u32x4_at2 *>(A.y + i) = u32x4{0, 0, 0, 0};
+        else
+            for (int64_t j = i; j < z1; j++) A.y[j] = 0;
     }
 }
 

@@ -43,11 +43,11 @@ __device__ __forceinline__ u32x2 to_fp8(const float (&x)[8], int c) {
 
 // 8 values of a row from column k on, zeros past its K columns
 template <bool kBf16>
-__device__ __forceinline__ void load_row8(const void *x, int64_t at, int64_t k, int64_t K, bool vec, float (&v)[8]) {
+__device__ __forceinline__ void load_row8(const void *x, int64_t at, int64_t k, int64_t K, float (&v)[8]) {
     if constexpr (kBf16) {
         const uint16_t *p = static_cast<const uint16_t *>(x) + at + k;
-        if (vec && k + 8 <= K) {
-            const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
+        if (k + 8 <= K) {
+            const u32x4 w = *reinterpret_cast<const u32x4_at2 *>(p);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 v[2 * j] = bf16_lo(w[j]);
@@ -59,8 +59,8 @@ __device__ __forceinline__ void load_row8(const void *x, int64_t at, int64_t k, 
         }
     } else {
         const float *p = static_cast<const float *>(x) + at + k;
-        if (vec && k + 8 <= K) {
-            const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
+        if (k + 8 <= K) {
+            const f32x4 a = reinterpret_cast<const f32x4_at4 *>(p)[0], b = reinterpret_cast<const f32x4_at4 *>(p)[1];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 v[j] = a[j];
@@ -83,8 +83,8 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 // q [M][128 kb], scale [M][sb]; sb is kb rounded up to 4, the bytes past kb are 127
 template <bool kBf16>
 __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const void *__restrict__ x, int64_t stride, int64_t M,
-                                                              int64_t K, int kb, int sb, bool vec,
-                                                              uint8_t *__restrict__ q, uint8_t *__restrict__ scale) {
+                                                              int64_t K, int kb, int sb, uint8_t *__restrict__ q,
+                                                              uint8_t *__restrict__ scale) {
     const int64_t u = (int64_t)blockIdx.x * kUnits + threadIdx.x / kUnitLanes;
     const int lane = threadIdx.x % kUnitLanes;
     const int64_t m = u / sb;
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const void *__rest
         return;
     }
     float v[8];
-    load_row8<kBf16>(x, m * stride, (int64_t)b * kScaleBlock + lane * 8, K, vec, v);
+    load_row8<kBf16>(x, m * stride, (int64_t)b * kScaleBlock + lane * 8, K, v);
     const int c = fp8_scale_code(row_max_f32(amax8(v)));
     *reinterpret_cast<u32x2 *>(q + (m * kb + b) * kScaleBlock + lane * 8) = to_fp8(v, c);
     if (lane == 0) scale[m * sb + b] = (uint8_t)c;
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const void *__rest
 // a value at most, against the 2^-4 of the rounding that follows): with exact
 // division and exponential, arithmetic bounds the pass, 199 us for 65536 x 2048.
 __global__ __launch_bounds__(kThreads) void swiglu_quant_kernel(const uint16_t *__restrict__ x, int64_t M, int64_t I,
-                                                                int kb, int sb, bool vec, uint8_t *__restrict__ q,
+                                                                int kb, int sb, uint8_t *__restrict__ q,
                                                                 uint8_t *__restrict__ scale) {
     const int64_t u = (int64_t)blockIdx.x * kUnits + threadIdx.x / kUnitLanes;
     const int lane = threadIdx.x % kUnitLanes;
@@ -118,8 +118,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_quant_kernel(const uint16_t *
         return;
     }
     float g[8], v[8];
-    load_row8<true>(x, m * 2 * I, (int64_t)b * kScaleBlock + lane * 8, I, vec, g);
-    load_row8<true>(x, m * 2 * I + I, (int64_t)b * kScaleBlock + lane * 8, I, vec, v);
+    load_row8<true>(x, m * 2 * I, (int64_t)b * kScaleBlock + lane * 8, I, g);
+    load_row8<true>(x, m * 2 * I + I, (int64_t)b * kScaleBlock + lane * 8, I, v);
 #pragma unroll
     for (int j = 0; j < 8; j++) v[j] *= g[j] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[j]));
     const int c = fp8_scale_code(row_max_f32(amax8(v)));
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_quant_kernel(const uint16_t *
 // transposed matrix [K][N up to 128] and its transposed scales.
 template <bool kBf16, bool kTrans>
 __global__ __launch_bounds__(kThreads) void quant_blocks_kernel(const void *__restrict__ w, int64_t group_stride,
-                                                                int64_t N, int64_t K, int nb, int kb, bool vec,
+                                                                int64_t N, int64_t K, int nb, int kb,
                                                                 uint8_t *__restrict__ q,
                                                                 uint8_t *__restrict__ scale) {
     __shared__ float top[kThreads / kWave];
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(kThreads) void quant_blocks_kernel(const void *__re
     for (int i = 0; i < 8; i++) {
         const int64_t n = (int64_t)bn * 128 + r0 + 16 * i;
         if (n < N) {
-            load_row8<kBf16>(w, g * group_stride + n * K, (int64_t)bk * 128 + c0, K, vec, v[i]);
+            load_row8<kBf16>(w, g * group_stride + n * K, (int64_t)bk * 128 + c0, K, v[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; j++) v[i][j] = 0.0f;
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(kThreads) void quant_blocks_kernel(const void *__re
 __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t *__restrict__ y, int64_t rows,
                                                            const int32_t *__restrict__ pos,
                                                            const float *__restrict__ weights, int64_t T, int k,
-                                                           int64_t H, int64_t chunks, bool vec,
+                                                           int64_t H, int64_t chunks,
                                                            uint16_t *__restrict__ out) {
     const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t t = u / chunks, h = (u - t * chunks) * 8;
@@ -196,13 +196,13 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t *__res
         if (p < 0 || p >= rows) continue;
         const float w = weights[t * k + j];
         float v[8];
-        load_row8<true>(y, (int64_t)p * H, h, H, vec, v);
+        load_row8<true>(y, (int64_t)p * H, h, H, v);
 #pragma unroll
         for (int i = 0; i < 8; i++) s[i] += w * v[i];
     }
     uint16_t *o = out + t * H + h;
-    if (vec && h + 8 <= H) {
-        *reinterpret_cast<u32x4 *>(o) =
+    if (h + 8 <= H) {
+        *reinterpret_cast<u32x4_at2 *>(o) =
             u32x4{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]), pack_bf16(s[6], s[7])};
     } else {
 #pragma unroll
@@ -234,11 +234,10 @@ extern "C" int ep_quant_rows(const void *x, int32_t dtype, int64_t rows, int64_t
         return EP_ERR_INVALID_ARG;
     const int kb = (int)ceil_div(cols, kScaleBlock), sb = (int)ep_scale_stride(cols);
     if (rows > (int64_t)1 << 40 || !fits_grid(rows * sb, kUnits)) return EP_ERR_INVALID_ARG;
-    const bool vec = is_aligned(x, 16) && (stride * width) % 16 == 0;
     const uint32_t grid = (uint32_t)ceil_div(rows * sb, kUnits);
     const hipStream_t s = to_stream(stream);
-    if (bf16) quant_rows_kernel<true><<<grid, kThreads, 0, s>>>(x, stride, rows, cols, kb, sb, vec, q, scale);
-    else quant_rows_kernel<false><<<grid, kThreads, 0, s>>>(x, stride, rows, cols, kb, sb, vec, q, scale);
+    if (bf16) quant_rows_kernel<true><<<grid, kThreads, 0, s>>>(x, stride, rows, cols, kb, sb, q, scale);
+    else quant_rows_kernel<false><<<grid, kThreads, 0, s>>>(x, stride, rows, cols, kb, sb, q, scale);
     return rc_of(hipGetLastError());
 }
 
@@ -250,9 +249,8 @@ extern "C" int ep_swiglu_quant(const void *gate_up, int64_t rows, int64_t inter,
         return EP_ERR_INVALID_ARG;
     const int kb = (int)ceil_div(inter, kScaleBlock), sb = (int)ep_scale_stride(inter);
     if (rows > (int64_t)1 << 40 || !fits_grid(rows * sb, kUnits)) return EP_ERR_INVALID_ARG;
-    const bool vec = is_aligned(gate_up, 16) && inter % 8 == 0;
     swiglu_quant_kernel<<<(uint32_t)ceil_div(rows * sb, kUnits), kThreads, 0, to_stream(stream)>>>(
-        static_cast<const uint16_t *>(gate_up), rows, inter, kb, sb, vec, q, scale);
+        static_cast<const uint16_t *>(gate_up), rows, inter, kb, sb, q, scale);
     return rc_of(hipGetLastError());
 }
 
@@ -266,11 +264,10 @@ extern "C" int ep_quant_blocks(const void *w, int32_t dtype, int32_t groups, int
     const bool bf16 = dtype == EP_DTYPE_BF16;
     const int width = bf16 ? 2 : 4;
     if (!w || !q || !scale || !is_aligned(w, width) || !is_aligned(q, 16)) return EP_ERR_INVALID_ARG;
-    const bool vec = is_aligned(w, 16) && (cols * width) % 16 == 0 && (groups == 1 || (group_stride * width) % 16 == 0);
     const dim3 grid((uint32_t)kb, (uint32_t)nb, (uint32_t)groups);
     const hipStream_t s = to_stream(stream);
     auto run = [&](auto kernel) {
-        kernel<<<grid, kThreads, 0, s>>>(w, group_stride, rows, cols, (int)nb, (int)kb, vec, q, scale);
+        kernel<<<grid, kThreads, 0, s>>>(w, group_stride, rows, cols, (int)nb, (int)kb, q, scale);
     };
     if (bf16) transpose ? run(quant_blocks_kernel<true, true>) : run(quant_blocks_kernel<true, false>);
     else transpose ? run(quant_blocks_kernel<false, true>) : run(quant_blocks_kernel<false, false>);
@@ -286,9 +283,8 @@ extern "C" int ep_moe_combine(const void *y, int64_t rows, const int32_t *pos, c
         return EP_ERR_INVALID_ARG;
     const int64_t chunks = ceil_div(hidden, 8);
     if (num_tokens > (int64_t)1 << 38 || !fits_grid(num_tokens * chunks, kThreads)) return EP_ERR_INVALID_ARG;
-    const bool vec = is_aligned(y, 16) && is_aligned(out, 16) && hidden % 8 == 0;
     combine_kernel<<<(uint32_t)ceil_div(num_tokens * chunks, kThreads), kThreads, 0, to_stream(stream)>>>(
-        static_cast<const uint16_t *>(y), rows, pos, weights, num_tokens, top_k, hidden, chunks, vec,
+        static_cast<const uint16_t *>(y), rows, pos, weights, num_tokens, top_k, hidden, chunks,
         static_cast<uint16_t *>(out));
     return rc_of(hipGetLastError());
 }
