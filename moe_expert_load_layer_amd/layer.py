@@ -217,6 +217,18 @@ def ep_quant_blocks(w: torch.Tensor, transpose: bool = False, q=None, scale=None
 def _matrix(data: torch.Tensor, scale: Optional[torch.Tensor], rows: int, cols: int, name: str) -> _CMatrix:
     """[experts][rows][cols] (bf16) or [experts][rows][cols up to 128] with scales (8 bits); experts may be apart."""
     fp8 = scale is not None
+    shape, stride = data.shape, data.stride()
+    if fp8:
+        blocks, width = (rows + 127) // 128, (cols + 127) // 128 * 128
+        if (data.is_cuda and data.dtype is _FP8 and len(shape) == 3 and shape[1] == rows and shape[2] == width and
+                stride[2] == 1 and stride[1] == width and scale.is_cuda and scale.dtype is torch.uint8 and
+                scale.shape == (shape[0], blocks, width // 128)):
+            ss = scale.stride()
+            if (ss[2] == 1 or width == 128) and (ss[1] == width // 128 or blocks == 1):
+                return _CMatrix(data.data_ptr(), scale.data_ptr(), stride[0], ss[0])
+    elif (data.is_cuda and data.dtype is torch.bfloat16 and len(shape) == 3 and shape[1] == rows and
+          shape[2] == cols and stride[2] == 1 and stride[1] == cols):
+        return _CMatrix(data.data_ptr(), None, stride[0] * 2, 0)
     if not data.is_cuda or data.dim() != 3 or data.dtype != (_FP8 if fp8 else torch.bfloat16):
         raise EPBalanceError(f"{name} must be a device tensor [experts][rows][cols] in "
                              f"{'float8_e4m3fn' if fp8 else 'bfloat16'}, got {data.dtype} {tuple(data.shape)}")
@@ -264,24 +276,22 @@ def ep_grouped_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w
     _arg(x, _FP8, x.shape, "x")
     _arg(x_scale, torch.uint8, (x.shape[0], ep_scale_stride(K)), "x_scale")
     G = _groups(offsets, layout, w.shape[0])
-    p = _CMatmul()
+    X = M = x.shape[0]
     if rows is not None:
         if rows.dim() != 1:
             raise EPBalanceError("rows must be [output rows]")
         _arg(rows, torch.int32, rows.shape, "rows")
-        p.rows = rows.data_ptr()
-    M = x.shape[0] if rows is None else rows.shape[0]
-    p.w = _matrix(w, w_scale, N, K, "w")
+        M = rows.shape[0]
+    y = _out(y, torch.bfloat16, (M, N), x.device, "y")
+    p = _CMatmul(x.data_ptr(), x_scale.data_ptr(), X, None if rows is None else rows.data_ptr(), rows_div, G,
+                 None if offsets is None else offsets.data_ptr(), M, N, K, _matrix(w, w_scale, N, K, "w"), _CMatrix(),
+                 None, y.data_ptr())
     if layout is not None:
         p.layout = ctypes.pointer(layout.c)
         if layout.num_spare:
             if slot_w is None or slot_w_scale is None or slot_w.shape[0] != layout.num_spare:
                 raise EPBalanceError(f"slot_w and slot_w_scale must hold the layout's {layout.num_spare} spare slots")
             p.slot_w = _matrix(slot_w, slot_w_scale, N, K, "slot_w")
-    y = _out(y, torch.bfloat16, (M, N), x.device, "y")
-    p.x, p.x_scale, p.x_rows, p.rows_div, p.groups = x.data_ptr(), x_scale.data_ptr(), x.shape[0], rows_div, G
-    p.offsets = None if offsets is None else offsets.data_ptr()
-    p.m, p.n, p.k, p.y = M, N, K, y.data_ptr()
     _check(lib().ep_grouped_matmul(ctypes.byref(p), _stream(stream)), "ep_grouped_matmul")
     return y
 
@@ -461,6 +471,7 @@ class AdamW:
             self.exp_avg_scale, self.exp_avg_sq_scale = (
                 [torch.ones((p.numel() + 127) // 128, dtype=torch.uint8, device=p.device) for p in self.params]
                 for _ in range(2))
+        self._scales = [((p.numel() + 127) // 128,) for p in self.params]
         # the library's descriptors, one a row, as the 8 words of ep_adamw_tensor_t
         self._words = np.zeros((len(self.params), 8), dtype=np.int64)
         self._words[:, 7] = [p.numel() for p in self.params]
@@ -469,29 +480,29 @@ class AdamW:
         """The descriptors' address; the lists above may have been given other tensors (a checkpoint's), so all are
         looked at."""
         state = torch.float32 if self.bits == 32 else torch.uint8
-        columns = [(0, self.params, torch.float32, "params"), (2, self.exp_avg, state, "exp_avg"),
+        params, words, eight = self.params, self._words, self.bits == 8
+        shapes = [p.shape for p in params]
+        columns = [(0, params, torch.float32, "params"), (2, self.exp_avg, state, "exp_avg"),
                    (3, self.exp_avg_sq, state, "exp_avg_sq")]
         if grads is not None:
             columns.append((1, grads, grads[0].dtype if grads else torch.float32, "grads"))
-        if self.copies is not None:
-            columns.append((6, self.copies, torch.bfloat16, "copies"))
-        shapes = [p.shape for p in self.params]
+            if self.copies is not None:
+                columns.append((6, self.copies, torch.bfloat16, "copies"))
+        if eight:
+            lengths = self._scales
+            columns += [(4, self.exp_avg_scale, torch.uint8, "exp_avg_scale"),
+                        (5, self.exp_avg_sq_scale, torch.uint8, "exp_avg_sq_scale")]
         for word, tensors, dtype, name in columns:
-            if len(tensors) != len(shapes):
-                raise EPBalanceError(f"{name} must be one for each of the {len(shapes)} parameters")
-            for i, (t, shape) in enumerate(zip(tensors, shapes)):
-                if not (t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
+            want = lengths if word in (4, 5) else shapes
+            if len(tensors) != len(want):
+                raise EPBalanceError(f"{name} must be one for each of the {len(want)} parameters")
+            if not all([t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
+                        for t, shape in zip(tensors, want)]):
+                for i, (t, shape) in enumerate(zip(tensors, want)):
                     _arg_or_raise(t, dtype, shape, f"{name}[{i}]")
-            if shapes:
-                self._words[:, word] = [t.data_ptr() for t in tensors]
-        if self.bits == 8:
-            for word, tensors, name in ((4, self.exp_avg_scale, "exp_avg_scale"),
-                                        (5, self.exp_avg_sq_scale, "exp_avg_sq_scale")):
-                for i, (t, p) in enumerate(zip(tensors, self.params)):
-                    _arg(t, torch.uint8, ((p.numel() + 127) // 128,), f"{name}[{i}]")
-                if shapes:
-                    self._words[:, word] = [t.data_ptr() for t in tensors]
-        return self._words.ctypes.data
+            if want:
+                words[:, word] = [t.data_ptr() for t in tensors]
+        return words.ctypes.data
 
     def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, grad_scale: float = 1.0,
              stream=None) -> None:
@@ -510,8 +521,17 @@ class AdamW:
         """(exp_avg, exp_avg_sq) as lists of float32 tensors: the moments themselves, or the 8-bit ones' values."""
         if self.bits == 32:
             return self.exp_avg, self.exp_avg_sq
-        m, v = ([torch.empty(p.shape, dtype=torch.float32, device=p.device) for p in self.params] for _ in range(2))
         n = len(self.params)
-        mp, vp = ((_vp * max(1, n))(*[t.data_ptr() for t in what]) for what in (m, v))
-        _check(lib().ep_adamw_values(self._tensors(), n, mp, vp, _stream(stream)), "ep_adamw_values")
-        return m, v
+        if n == 0:
+            return [], []
+        # the values of all tensors lie one after the other in one piece of memory
+        sizes = self._words[:, 7]
+        flat = torch.empty((2, int(sizes.sum())), dtype=torch.float32, device=self.params[0].device)
+        out = []
+        for part in flat.unbind():
+            out.append([t if p.dim() == 1 else t.view(p.shape) for t, p in zip(part.split(sizes.tolist()), self.params)])
+        mp = flat.data_ptr() + 4 * (np.cumsum(sizes) - sizes)
+        vp = mp + 4 * flat.shape[1]
+        _check(lib().ep_adamw_values(self._tensors(), n, mp.ctypes.data, vp.ctypes.data, _stream(stream)),
+               "ep_adamw_values")
+        return out[0], out[1]
