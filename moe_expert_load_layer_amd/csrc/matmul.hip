@@ -433,9 +433,9 @@ extern "C" int ep_grouped_matmul(const ep_grouped_matmul_t *p, ep_stream_t strea
     const hipStream_t s = to_stream(stream);
     // The largest tile whose groups mostly fill it and whose count fills the card
     // (about 200 tiles).  Measured, us for 8 groups of N = K = 4096 with tiles of
-    // 256 x 256, 128 x 128, 64 x 64: 400 rows a group 64, 91, 139; 200 rows 56, 54,
-    // 79; 50 rows 44, 29, 38; 20 rows 44, 28, 25.  One group of 2048 x 2048 x 2048:
-    // 30, 20, 29; of 1024 x 1024 x 4096: 43, 22, 17.
+    // 256 x 256, 128 x 128, 64 x 64: 400 rows a group 61, 79, 117; 200 rows 45, 42,
+    // 61; 50 rows 42, 25, 24; 20 rows 42, 25, 23.  One group of 2048 x 2048 x 2048:
+    // 26, 15, 22; of 1024 x 1024 x 4096: 40, 19, 14; of 4096 x 4096 x 2048: 36, 44, 74.
     const int64_t rows = p->m / p->groups;
     auto enough = [&](int64_t tile) { return ceil_div(p->m, tile) * ceil_div(p->n, tile) >= 192; };
     if (rows >= 256 && enough(256)) return rc_of(launch<256, 256, 64, 128, 4>(A, s));
