@@ -2,13 +2,15 @@
 //   up    gate (gate.h), then h_p = silu(Wg_e x_t) * (Wu_e x_t) for every pair p = (t, j), e = id_tj
 //   down  out_t = sum_j w_tj Wd_e h_p
 //
+// With more than 32 tokens the gate is a launch of its own before them.
+//
 // Bound: HBM.  Every distinct expert's three matrices are read once, which is
 // all but a fraction of a percent of the bytes.  (With more than 8 tokens, gate
 // and up are read once for every 32 tokens of an expert and down once for every
 // 16: more columns would leave LDS for fewer workgroups.)
 // Measured, up and down: 1 token, 8 of 128 experts, 4096 x 1536 in bf16 44 + 22 us
 // (302 MB, 4.6 TB/s); 7 tokens, 7168 x 2048 in 8 bits 173 + 93 us (1.40 GB, 5.3);
-// 61 tokens, 160 experts, 5120 x 1536 in bf16 526 + 279 us (4.34 GB, 5.4).
+// 61 tokens, 160 experts, 5120 x 1536 in bf16 5 + 509 + 275 us (4.34 GB, 5.5).
 //
 // Both kernels stream: a workgroup takes 64 weight rows of an expert and walks
 // them in windows of 128 bytes a row, together with the same window of the
@@ -29,6 +31,8 @@
 // 8-bit weights: a window is 128 values with one scale byte; v_cvt_scalef32
 // gives bf16 exactly (3 bits of mantissa, power-of-two scale), so products and
 // sums are those of the bf16 path.
+#include <math.h>
+
 #include "gate.h"
 #include "groups.h"
 
@@ -46,6 +50,7 @@ constexpr int kWindowBytes = 128;      // of one row
 constexpr int kScaleUnits = 512;       // windows whose scale bytes are in LDS at a time
 // pairs of one expert that are multiplied together: 8 where no expert can have more
 constexpr int kFew = 8, kUpMany = 32, kDownMany = 16;
+constexpr int kGateAlone = 32;  // tokens up to which the first kernel chooses for itself
 constexpr int kMaxEntries = kGateMaxExperts + kMaxPairs / kDownMany;
 
 __device__ __align__(16) const uint32_t kNothing[4] = {0, 0, 0, 0};
@@ -62,6 +67,7 @@ struct FewArgs {
     int64_t x_stride, out_stride;  // elements
     Matrix wg, wu, wd;
     int32_t T, H, I, k;
+    bool chosen;  // ids and weights are there already
     int32_t *ids;
     float *weights;
     uint16_t *out;
@@ -131,7 +137,7 @@ __device__ void build_lists(Lists *L, Scratch *W, int T, int k, int E) {
 }
 
 template <bool kFp8>
-__device__ __forceinline__ int windows_of(int K) {
+__host__ __device__ __forceinline__ int windows_of(int K) {
     return kFp8 ? (K + 127) / 128 : (K + 63) / 64;
 }
 
@@ -261,9 +267,11 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const FewArgs A) {
     __shared__ uint8_t scales[kFp8 ? 2 * kScaleUnits : 2];
     static_assert(sizeof(Scratch) <= sizeof(stages), "the scratch fits the stages");
     Scratch *W = reinterpret_cast<Scratch *>(stages);
-    // every workgroup chooses for itself; the first one writes the choice
+    // every workgroup chooses for itself, and the first one writes the choice
     constexpr int kPass = kThreads / kGateLanes;
-    for (int t0 = 0; t0 < A.T; t0 += kPass) {
+    if (A.chosen)
+        for (int p = threadIdx.x; p < A.T * A.k; p += kThreads) W->ids[p] = A.ids[p];
+    for (int t0 = 0; t0 < A.T && !A.chosen; t0 += kPass) {
         const int s = threadIdx.x / kGateLanes, j = threadIdx.x % kGateLanes, t = t0 + s;
         int id;
         float w;
@@ -375,12 +383,22 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const FewArgs A) {
     wait_loads();  // those that nobody reads
 }
 
-// Shares of the weights that the workgroups of one block of output rows take:
-// about 512 workgroups in all, shares of 4 windows at least.
-int down_shares(int T, int k, int H, int I) {
+// Shares of the weights that the workgroups of one block of output rows take, at
+// most: about 512 workgroups in all, shares of 4 windows at least.
+int most_shares(int T, int k, int H, int I) {
     const int64_t blocks = ceil_div(H, kRows), windows = (int64_t)T * k * ceil_div(I, 64);
     const int64_t want = 512 / blocks < windows / 4 ? 512 / blocks : windows / 4;
     return want < 1 ? 1 : want > 32 ? 32 : (int)want;
+}
+
+// The shares of a call.  A block's W windows of 8 KiB take W / s of a share's
+// time, and adding s shares of 256 T bytes takes s T / 32: their sum is least at
+// s = sqrt(32 W / T).  (63 tokens, 16 experts, 416 x 384: 22.6 us with the rule above
+// alone, 19.8 with this one.)
+int down_shares(const FewArgs &A, int windows, int cols) {
+    const int pairs = A.T * A.k, entries = (A.gate.E < pairs ? A.gate.E : pairs) + pairs / cols;
+    const int best = (int)sqrt(32.0 * entries * windows / A.T), most = most_shares(A.T, A.k, A.H, A.I);
+    return best < 1 ? 1 : best < most ? best : most;
 }
 
 __device__ __forceinline__ void store_past_l2(uint64_t *p, float a, float b) {
@@ -573,7 +591,7 @@ hipError_t launch(const FewArgs &A, hipStream_t s) {
     const hipError_t e = hipLaunchKernel(up, dim3((uint32_t)blocks), dim3(kThreads), args, 0, s);
     if (e != hipSuccess) return e;
     return hipLaunchKernel((const void *)down_kernel<kFp8, kDownCols>,
-                           dim3((uint32_t)ceil_div(A.H, kRows), down_shares(A.T, A.k, A.H, A.I)), dim3(kThreads), args,
+                           dim3((uint32_t)ceil_div(A.H, kRows), down_shares(A, windows_of<kFp8>(A.I), kDownCols)), dim3(kThreads), args,
                            (size_t)kWaves * A.T * 16 * sizeof(float), s);
 }
 
@@ -611,7 +629,7 @@ Parts parts_of(int32_t T, int32_t k, int32_t H, int32_t I) {
     p.low = (size_t)T * k * I * sizeof(uint16_t);  // a multiple of 16: I is one of 8
     p.arrivals = align256(2 * p.low);
     p.sums = p.arrivals + align256((size_t)ceil_div(H, kRows) * sizeof(int32_t));
-    p.total = p.sums + (size_t)down_shares(T, k, H, I) * T * H * sizeof(float);
+    p.total = p.sums + (size_t)most_shares(T, k, H, I) * T * H * sizeof(float);
     return p;
 }
 
@@ -667,5 +685,13 @@ extern "C" int ep_moe_few_tokens(const void *x, int64_t x_stride, int32_t num_to
     A.hlo = reinterpret_cast<uint16_t *>(w + parts.low);
     A.arrivals = reinterpret_cast<int32_t *>(w + parts.arrivals);
     A.sums = reinterpret_cast<float *>(w + parts.sums);
+    // With many tokens the gate runs by itself first, where each workgroup would take
+    // 3 us for every 16 of them.  Measured, in the first kernel or before it: 63 tokens
+    // 25 us, 6 + 10; 40 tokens 35, 5 + 29; 24 tokens 25, 4 + 21.
+    A.chosen = num_tokens > kGateAlone;
+    if (A.chosen) {
+        const int rc = ep_gate_topk(logits, logits_stride, num_tokens, gate, ids, weights, stream);
+        if (rc != EP_OK) return rc;
+    }
     return rc_of(fp8 ? launch<true>(A, to_stream(stream)) : launch<false>(A, to_stream(stream)));
 }
