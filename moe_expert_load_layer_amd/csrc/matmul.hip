@@ -128,11 +128,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
     constexpr int kStage = (BM + BN) * kStep;
     constexpr int kChunk = BM * kScaleBlocks + kWScaleBytes;  // bytes of a chunk of scales: of x, then of w
     constexpr int kScaleLoads = BM * (kScaleBlocks / 4) / kThreads;
-    constexpr int kStores = FM * FN * 2;  // 16-byte stores of a lane for a full tile
     static_assert((BM + BN) % (kLoadRows * kWaves) == 0 && BM % kLoadRows == 0, "whole loads");
     static_assert(BM * (kScaleBlocks / 4) % kThreads == 0 && BM <= kThreads, "whole loads of scales");
     static_assert(kScaleBlock % WN == 0 && BN <= 2 * kScaleBlock, "a wave's columns share a scale");
-    static_assert(kStages % 2 == 0 && (kStages - 2) * kLoads + kStores < 64, "steps go in pairs; a wait's largest count");
+    static_assert(kStages % 2 == 0 && (kStages - 2) * kLoads < 64, "steps go in pairs; a wait's largest count");
     __shared__ __align__(16) uint8_t stages[kStages * kStage];
     __shared__ __align__(16) uint8_t scales[3 * kChunk];
     // This tile and the next one, in LDS rather than in registers: a tile's rows and
@@ -386,7 +385,6 @@ hipError_t launch(const MatmulArgs &A, hipStream_t s) {
 }
 
 }  // namespace
-
 }  // namespace ep
 
 using namespace ep;
