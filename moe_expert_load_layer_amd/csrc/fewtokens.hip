@@ -590,8 +590,8 @@ hipError_t launch(const FewArgs &A, hipStream_t s) {
     void *args[] = {const_cast<FewArgs *>(&A)};
     const hipError_t e = hipLaunchKernel(up, dim3((uint32_t)blocks), dim3(kThreads), args, 0, s);
     if (e != hipSuccess) return e;
-    return hipLaunchKernel((const void *)down_kernel<kFp8, kDownCols>,
-                           dim3((uint32_t)ceil_div(A.H, kRows), down_shares(A, windows_of<kFp8>(A.I), kDownCols)), dim3(kThreads), args,
+    const dim3 grid((uint32_t)ceil_div(A.H, kRows), down_shares(A, windows_of<kFp8>(A.I), kDownCols));
+    return hipLaunchKernel((const void *)down_kernel<kFp8, kDownCols>, grid, dim3(kThreads), args,
                            (size_t)kWaves * A.T * 16 * sizeof(float), s);
 }
 

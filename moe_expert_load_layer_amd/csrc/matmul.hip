@@ -173,8 +173,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
         int g = 0, first = 0;
         find_tile(A.groups, BM, tile, &g, &first);
         Tile t;
-        t.m0 = A.groups.start(g) + (tile - first) * BM;
+        // inside the group also where groups that overlap have more tiles than an int counts
+        const int start = A.groups.start(g);
         t.m1 = A.groups.end(g);
+        t.m0 = start + min(max(tile - first, 0), max(t.m1 - start - 1, 0) / BM) * BM;
         t.n0 = tn * BN;
         int row;
         const bool spare = A.where.spare(g, &row);
@@ -182,7 +184,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
         t.ws = spare ? A.slot_ws + row * A.slot_ws_stride : A.ws + row * A.ws_stride;
         if (thread == 0) tiles[buf] = t;
         if (thread < BM) {
-            int r = min(t.m0 + thread, t.m1 - 1);  // rows past the end repeat the last
+            int r = max(min(t.m0 + thread, t.m1 - 1), 0);  // rows past the end repeat the last
             if (A.rows) {
                 const int p = A.rows[r];
                 r = p < 0 ? -1 : p / A.rows_div;
