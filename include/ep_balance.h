@@ -468,7 +468,8 @@ typedef struct ep_matrix {
  * consecutive rows offsets[g] .. offsets[g + 1] - 1, offsets[0] = 0.  Rows from
  * offsets[groups] on become 0.  Offsets live on the device and cannot be refused:
  * values outside [0, m] are brought into it and a group that ends before its start
- * is empty, so that no access leaves a buffer.
+ * is empty, so that no access leaves a buffer.  Groups that overlap for that
+ * reason each multiply their rows; a row of several holds one of their products.
  *   x, x_scale  as ep_quant_rows writes them: k columns, x_rows rows
  *   rows        device int32 [m] or NULL: r(i) = rows[i] / rows_div (the pair
  *               that a dispatch position serves, rows_div = top-k); a negative

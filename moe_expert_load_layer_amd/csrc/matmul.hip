@@ -25,6 +25,7 @@
 // scales; zeros instead of random values take a fifth less, as the card lowers
 // its clock (2.4 GHz to 1.8) under this load.
 #include "groups.h"
+#include "walk.h"
 
 namespace ep {
 namespace {
@@ -116,10 +117,12 @@ __device__ __forceinline__ void matmul_step(const uint8_t *next, uint32_t fill, 
 // tile's last steps fetch the first ones of the next.  Finding a tile, its rows'
 // places, the first loads and the wait for them, and the stores of the tile
 // before cost 12 us a tile where each of them had a workgroup of its own.
+// kChained false: the steps are too few for that (walk.h), a workgroup has one
+// tile, or begins again where groups overlap and there are more.
 //
 // kStages: the next step's stage, those in flight, and this step's, whose
 // operands are in registers and which is filled again.
-template <int BM, int BN, int WM, int WN, int kStages>
+template <int BM, int BN, int WM, int WN, int kStages, bool kChained>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kernel(const MatmulArgs A) {
     constexpr int kWavesM = BM / WM, kWaves = kWavesM * (BN / WN), kThreads = kWaves * kWave;
     constexpr int FM = WM / 32, FN = WN / 32;
@@ -143,16 +146,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
     __shared__ Tile tiles[2];
     __shared__ int32_t places[2][BM];
 
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave % kWavesM, wn = wave / kWavesM;
     const int nt = (A.N + BN - 1) / BN;
     const int mt = __builtin_amdgcn_readfirstlane(total_tiles(A.groups, BM));  // kept in a scalar register
-    // the workgroups of one XCD (consecutive ones go round the 8 XCDs) take
-    // consecutive tiles: 4 row tiles by all column tiles, columns last, so that
-    // the tiles in flight on an XCD share rows of x and of w in its L2
-    const int64_t all = (int64_t)mt * nt, per = (all + 7) / 8;
-    const int64_t from = blockIdx.x % 8 * per, to = min(from + per, all);
-    const int stride = gridDim.x / 8;
+    // an XCD's consecutive tiles: 4 row tiles by all column tiles, columns last, so
+    // that the tiles in flight there share rows of x and of w in its L2
+    const TileWalk walk = tile_walk((int64_t)mt * nt, blockIdx.x, gridDim.x);
     const int64_t row_bytes = (int64_t)A.kb * 128;
     const int steps = A.kb * kParts;  // even
 
@@ -224,32 +224,38 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
         load_lds_bytes(t.ws + (int64_t)nb * A.kb + min(b0 + l % kScaleBlocks, A.kb - 1), to + BM * kScaleBlocks);
     };
 
-    int64_t at = from + blockIdx.x / 8;
-    if (at < to) {
+    int64_t at = walk.at;
+    if (at < walk.to) {
         const uint32_t ring = lds_address(stages) + wave * 1024;
         int buf = 0, slot = 0, chunk0 = 0;  // chunk0: where the tile's first chunk of scales lies
-        locate(at, buf);
-        sources(buf);
-        scale_loads(buf, 0, chunk0);
-#pragma unroll
-        for (int p = 0; p < kStages; p++)
-#pragma unroll
-            for (int i = 0; i < kLoads; i++) {
-                load_lds_1k(src[i], stages + p * kStage + (wave + i * kWaves) * 1024);
-                src[i] += p + 1 < steps ? kStep : 0;
-            }
-        wait_loads_but<(kStages - 1) * kLoads>();
-        __syncthreads();
         f32x16 acc[FN][FM];
         i32x8 fx[FM], fx2[FM], fw[FN];
-        int sx[FM], sx2[FM], sw = scales[BM * kScaleBlocks + wn * WN / kScaleBlock * kScaleBlocks * 4];
+        int sx[FM], sx2[FM], sw;
+        // a tile from nothing: fills the ring and reads the first step's operands
+        auto begin = [&] {
+            const int l = lane_now();
+            locate(at, buf);
+            sources(buf);
+            scale_loads(buf, 0, chunk0);
 #pragma unroll
-        for (int j = 0; j < FM; j++) {
-            fx[j] = read_frag(stages, wm * WM + j * 32 + (l & 31));
-            sx[j] = scales[scale_at(wm * WM + (l & 31), 0) + j * 32 * kScaleBlocks];
-        }
+            for (int p = 0; p < kStages; p++)
 #pragma unroll
-        for (int i = 0; i < FN; i++) fw[i] = read_frag(stages, BM + wn * WN + i * 32 + (l & 31));
+                for (int i = 0; i < kLoads; i++) {
+                    load_lds_1k(src[i], stages + p * kStage + (wave + i * kWaves) * 1024);
+                    src[i] += p + 1 < steps ? kStep : 0;
+                }
+            wait_loads_but<(kStages - 1) * kLoads>();
+            __syncthreads();
+            sw = scales[BM * kScaleBlocks + wn * WN / kScaleBlock * kScaleBlocks * 4];
+#pragma unroll
+            for (int j = 0; j < FM; j++) {
+                fx[j] = read_frag(stages, wm * WM + j * 32 + (l & 31));
+                sx[j] = scales[scale_at(wm * WM + (l & 31), 0) + j * 32 * kScaleBlocks];
+            }
+#pragma unroll
+            for (int i = 0; i < FN; i++) fw[i] = read_frag(stages, BM + wn * WN + i * 32 + (l & 31));
+        };
+        begin();
         for (;;) {
 #pragma unroll
             for (int i = 0; i < FN; i++)
@@ -257,7 +263,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
                 for (int j = 0; j < FM; j++)
 #pragma unroll
                     for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
-            const bool more = at + stride < to;
+            const bool more = at + walk.stride < walk.to;
             const int chunks = (A.kb + kScaleBlocks - 1) / kScaleBlocks;
             int ahead = kStep;
             // A step: its operands are in x, c and fw, the next one's (block `block` of
@@ -281,12 +287,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
                     const int ch = s / (kParts * kScaleBlocks) + 1;
                     if (ch < chunks) scale_loads(buf, ch, (chunk0 + ch) % 3);
                 }
-                if (more && s == steps - kStages - 4) {
-                    locate(at + stride, buf ^ 1);
+                if (kChained && more && s == find_step(steps, kStages)) {
+                    locate(at + walk.stride, buf ^ 1);
                     scale_loads(buf ^ 1, 0, (chunk0 + chunks) % 3);
                 }
                 if (s == max(steps - kStages, 0)) {  // from here on steps of the next tile are fetched
-                    if (more) {
+                    if (kChained && more) {
                         sources(buf ^ 1);
                     } else {  // or bytes that nobody reads, so that the count of loads stays
                         ahead = 0;
@@ -299,7 +305,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
                 const int here = (chunk0 + ch) % 3 * kChunk, there = (chunk0 + ch + 1) % 3 * kChunk;
                 int stop = end;
                 if (s < steps - kStages) stop = min(stop, steps - kStages);
-                if (more && s < steps - kStages - 4) stop = min(stop, steps - kStages - 4);
+                if (kChained && more && s < find_step(steps, kStages)) stop = min(stop, find_step(steps, kStages));
                 for (int b = s / kParts % kScaleBlocks; s < stop; s += 2, b++) {
                     step(here, b, fx, fx2, sx, sx2);  // the second half of this block
                     const bool last = s + 2 == end;
@@ -349,9 +355,15 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
                 }
             }
             if (!more) break;
-            at += stride;
+            at += walk.stride;
             buf ^= 1;
             chunk0 = (chunk0 + chunks) % 3;
+            if constexpr (!kChained) {
+                slot = chunk0 = 0;
+                wait_loads();
+                __syncthreads();  // every wave's, before the ring is filled again
+                begin();
+            }
         }
         wait_loads();  // those that nobody reads
     }
@@ -370,19 +382,17 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, 2) void matmul_kerne
 template <int BM, int BN, int WM, int WN, int kStages>
 hipError_t launch(const MatmulArgs &A, hipStream_t s) {
     constexpr int kThreads = (BM / WM) * (BN / WN) * kWave;
-    // every group may end in a part tile
-    const int64_t mt = A.groups.M / BM + A.groups.G;
-    int64_t blocks = ceil_div(mt * ceil_div(A.N, BN), 8) * 8;
-    // As many workgroups as the card holds; each its own tile where a tile's steps
-    // are too few: the next tile is found kStages + 4 steps before the end, and not
-    // before a barrier after the last tile's stores.
-    const void *kernel = (const void *)matmul_kernel<BM, BN, WM, WN, kStages>;
-    if (A.kb * kParts > kStages + 4) {
-        const int64_t resident = resident_blocks(kernel, kThreads, 0) / 8 * 8;
+    int64_t blocks = tile_blocks(A.groups.M, A.groups.G, A.N, BM, BN);
+    // As many workgroups as the card holds; where a tile's steps are too few to be
+    // chained, as many as there are tiles.
+    const auto kernel = tiles_chained(A.kb * kParts, kStages) ? matmul_kernel<BM, BN, WM, WN, kStages, true>
+                                                              : matmul_kernel<BM, BN, WM, WN, kStages, false>;
+    if (tiles_chained(A.kb * kParts, kStages)) {
+        const int64_t resident = resident_blocks((const void *)kernel, kThreads, 0) / 8 * 8;
         if (resident > 0 && resident < blocks) blocks = resident;
     }
     if (blocks > 0xffffffffll / kThreads) return hipErrorInvalidConfiguration;
-    matmul_kernel<BM, BN, WM, WN, kStages><<<(uint32_t)blocks, kThreads, 0, s>>>(A);
+    kernel<<<(uint32_t)blocks, kThreads, 0, s>>>(A);
     return hipGetLastError();
 }
 
