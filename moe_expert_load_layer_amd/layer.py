@@ -99,6 +99,14 @@ def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
+def _held(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory that a call takes from torch's allocator, which hands it out for the current stream: where the call runs
+    on another one, it is not handed out again before that stream has passed the call."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _rows(t: torch.Tensor, dtypes, name: str) -> int:
     """A device matrix whose rows are contiguous; returns its row stride."""
     if t.is_cuda and t.dtype in dtypes and t.dim() == 2:
@@ -379,7 +387,8 @@ def ep_moe_few_tokens(x: torch.Tensor, logits: torch.Tensor, k: int, gate: torch
     weights = _out(weights, torch.float32, (T, k), x.device, "weights")
     g = _gate(E, k, bias, num_groups, topk_groups, scale, logits.dtype)
     if ws is None:
-        ws = torch.empty(max(16, ep_few_tokens_workspace_bytes(T, k, H, I)), dtype=torch.uint8, device=x.device)
+        ws = _held(torch.empty(max(16, ep_few_tokens_workspace_bytes(T, k, H, I)), dtype=torch.uint8,
+                               device=x.device), stream)
     elif not (ws.is_cuda and ws.is_contiguous()):
         raise EPBalanceError("ws must be a contiguous device tensor")
     rc = lib().ep_moe_few_tokens(_ptr(x), xs, T, _ptr(logits), ls, ctypes.byref(g), ctypes.byref(e), _ptr(out), H,

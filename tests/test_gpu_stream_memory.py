@@ -1,0 +1,43 @@
+"""Calls on a stream= that is not the current one, with memory that they allocate: while that stream is still busy,
+the current one takes and overwrites whatever the allocator hands out."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+ep = pytest.importorskip("moe_expert_load_layer_amd")
+
+BUSY = 20_000_000       # cycles of a bounded wait, about 10 ms
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def _behind(dev, call):
+    """call(side stream) behind a wait on it, the current stream overwriting freed memory meanwhile."""
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    out = call(side)
+    taken = [torch.full((size,), 255, dtype=torch.uint8, device=dev) for size in (1 << 9, 1 << 13, 1 << 16, 1 << 20)
+             for _ in range(24)]
+    torch.cuda.current_stream().synchronize()
+    side.synchronize()
+    assert all((t == 255).all() for t in taken)
+    return out
+
+
+def test_layer_for_a_few_tokens(dev):
+    E, H, I, T, k = 16, 512, 256, 5, 4
+    g = torch.Generator(device=dev).manual_seed(3)
+    w = [torch.randn(s, generator=g, device=dev).to(torch.bfloat16) / 10 for s in ((E, I, H), (E, I, H), (E, H, I))]
+    x = torch.randn((T, H), generator=g, device=dev).to(torch.bfloat16)
+    logits = torch.randn((T, E), generator=g, device=dev)
+    ref = ep.ep_moe_few_tokens(x, logits, k, *w)
+    got = _behind(dev, lambda s: ep.ep_moe_few_tokens(x, logits, k, *w, stream=s))
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
