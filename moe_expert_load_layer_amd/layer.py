@@ -128,9 +128,9 @@ def _rows(t: torch.Tensor, dtypes, name: str) -> int:
     return t.stride(0)
 
 
-def _out(t: Optional[torch.Tensor], dtype: torch.dtype, shape, device, name: str) -> torch.Tensor:
+def _out(t: Optional[torch.Tensor], dtype: torch.dtype, shape, device, name: str, stream) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _held(torch.empty(shape, dtype=dtype, device=device), stream)
     return _arg(t, dtype, shape, name)
 
 
@@ -146,8 +146,8 @@ def ep_gate_topk(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = No
     """logits fp32 or bf16 [T][E] -> (ids int32 [T][k], weights float32 [T][k])."""
     stride = _rows(logits, (torch.float32, torch.bfloat16), "logits")
     T, E = logits.shape
-    ids = _out(ids, torch.int32, (T, k), logits.device, "ids")
-    weights = _out(weights, torch.float32, (T, k), logits.device, "weights")
+    ids = _out(ids, torch.int32, (T, k), logits.device, "ids", stream)
+    weights = _out(weights, torch.float32, (T, k), logits.device, "weights", stream)
     g = _gate(E, k, bias, num_groups, topk_groups, scale, logits.dtype)
     rc = lib().ep_gate_topk(_ptr(logits), stride, T, ctypes.byref(g), _ptr(ids), _ptr(weights), _stream(stream))
     _check(rc, "ep_gate_topk")
@@ -165,7 +165,7 @@ def ep_gate_topk_backward(ids: torch.Tensor, weights: torch.Tensor, grad_weights
     _arg(ids, torch.int32, (T, k), "ids")
     _arg(weights, torch.float32, (T, k), "weights")
     _arg(grad_weights, torch.float32, (T, k), "grad_weights")
-    grad_logits = _out(grad_logits, dtype, (T, num_experts), ids.device, "grad_logits")
+    grad_logits = _out(grad_logits, dtype, (T, num_experts), ids.device, "grad_logits", stream)
     g = _gate(num_experts, k, None, 1, 1, scale, dtype)
     rc = lib().ep_gate_topk_backward(_ptr(ids), _ptr(weights), _ptr(grad_weights), T, ctypes.byref(g),
                                      _ptr(grad_logits), _stream(stream))
@@ -186,8 +186,8 @@ def ep_quant_rows(x: torch.Tensor, q=None, scale=None, stream=None):
     """x fp32 or bf16 [M][K] -> (q float8_e4m3fn [M][K up to 128], scale uint8 [M][ep_scale_stride(K)])."""
     stride = _rows(x, (torch.float32, torch.bfloat16), "x")
     M, K = x.shape
-    q = _out(q, _FP8, (M, _up128(K)), x.device, "q")
-    scale = _out(scale, torch.uint8, (M, ep_scale_stride(K)), x.device, "scale")
+    q = _out(q, _FP8, (M, _up128(K)), x.device, "q", stream)
+    scale = _out(scale, torch.uint8, (M, ep_scale_stride(K)), x.device, "scale", stream)
     _check(lib().ep_quant_rows(_ptr(x), _FLOATS[x.dtype], M, K, stride, _ptr(q), _ptr(scale), _stream(stream)),
            "ep_quant_rows")
     return q, scale
@@ -199,8 +199,8 @@ def ep_swiglu_quant(gate_up: torch.Tensor, q=None, scale=None, stream=None):
         raise EPBalanceError(f"gate_up must be [rows][2 * inter], got shape {tuple(gate_up.shape)}")
     M, I = gate_up.shape[0], gate_up.shape[1] // 2
     _arg(gate_up, torch.bfloat16, (M, 2 * I), "gate_up")
-    q = _out(q, _FP8, (M, _up128(I)), gate_up.device, "q")
-    scale = _out(scale, torch.uint8, (M, ep_scale_stride(I)), gate_up.device, "scale")
+    q = _out(q, _FP8, (M, _up128(I)), gate_up.device, "q", stream)
+    scale = _out(scale, torch.uint8, (M, ep_scale_stride(I)), gate_up.device, "scale", stream)
     _check(lib().ep_swiglu_quant(_ptr(gate_up), M, I, _ptr(q), _ptr(scale), _stream(stream)), "ep_swiglu_quant")
     return q, scale
 
@@ -214,8 +214,8 @@ def ep_quant_blocks(w: torch.Tensor, transpose: bool = False, q=None, scale=None
     if G and not w[0].is_contiguous():
         raise EPBalanceError("w must have contiguous matrices")
     a, b = (K, N) if transpose else (N, K)
-    q = _out(q, _FP8, (G, a, _up128(b)), w.device, "q")
-    scale = _out(scale, torch.uint8, (G, _up128(a) // 128, _up128(b) // 128), w.device, "scale")
+    q = _out(q, _FP8, (G, a, _up128(b)), w.device, "q", stream)
+    scale = _out(scale, torch.uint8, (G, _up128(a) // 128, _up128(b) // 128), w.device, "scale", stream)
     rc = lib().ep_quant_blocks(_ptr(w), _FLOATS[w.dtype], G, w.stride(0), N, K, int(transpose), _ptr(q), _ptr(scale),
                                _stream(stream))
     _check(rc, "ep_quant_blocks")
@@ -290,7 +290,7 @@ def ep_grouped_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w
             raise EPBalanceError("rows must be [output rows]")
         _arg(rows, torch.int32, rows.shape, "rows")
         M = rows.shape[0]
-    y = _out(y, torch.bfloat16, (M, N), x.device, "y")
+    y = _out(y, torch.bfloat16, (M, N), x.device, "y", stream)
     p = _CMatmul(x.data_ptr(), x_scale.data_ptr(), X, None if rows is None else rows.data_ptr(), rows_div, G,
                  None if offsets is None else offsets.data_ptr(), M, N, K, _matrix(w, w_scale, N, K, "w"), _CMatrix(),
                  None, y.data_ptr())
@@ -321,7 +321,7 @@ def ep_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: Optional[torch.
 
     def gradient(t, count, name):
         if t is None:
-            return torch.empty((count, N, K), dtype=torch.float32, device=dy.device)
+            return _held(torch.empty((count, N, K), dtype=torch.float32, device=dy.device), stream)
         if not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != (count, N, K):
             raise EPBalanceError(f"{name} must be a float32 device tensor of shape {(count, N, K)}")
         if count and not t[0].is_contiguous():
@@ -348,7 +348,7 @@ def ep_moe_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, ou
     _arg(pos, torch.int32, pos.shape, "pos")
     _arg(weights, torch.float32, pos.shape, "weights")
     (T, k), H = pos.shape, y.shape[1]
-    out = _out(out, torch.bfloat16, (T, H), y.device, "out")
+    out = _out(out, torch.bfloat16, (T, H), y.device, "out", stream)
     _check(lib().ep_moe_combine(_ptr(y), y.shape[0], _ptr(pos), _ptr(weights), T, k, H, _ptr(out), _stream(stream)),
            "ep_moe_combine")
     return out
@@ -382,9 +382,9 @@ def ep_moe_few_tokens(x: torch.Tensor, logits: torch.Tensor, k: int, gate: torch
             raise EPBalanceError(f"{name} must hold the {E} experts of the logits, got shape {tuple(t.shape)}")
     e = _CExperts(H, I, EP_DTYPE_BF16 if gate_scale is None else EP_DTYPE_FP8, _matrix(gate, gate_scale, I, H, "gate"),
                   _matrix(up, up_scale, I, H, "up"), _matrix(down, down_scale, H, I, "down"))
-    out = _out(out, torch.bfloat16, (T, H), x.device, "out")
-    ids = _out(ids, torch.int32, (T, k), x.device, "ids")
-    weights = _out(weights, torch.float32, (T, k), x.device, "weights")
+    out = _out(out, torch.bfloat16, (T, H), x.device, "out", stream)
+    ids = _out(ids, torch.int32, (T, k), x.device, "ids", stream)
+    weights = _out(weights, torch.float32, (T, k), x.device, "weights", stream)
     g = _gate(E, k, bias, num_groups, topk_groups, scale, logits.dtype)
     if ws is None:
         ws = _held(torch.empty(max(16, ep_few_tokens_workspace_bytes(T, k, H, I)), dtype=torch.uint8,
@@ -535,7 +535,7 @@ class AdamW:
             return [], []
         # the values of all tensors lie one after the other in one piece of memory
         sizes = self._words[:, 7]
-        flat = torch.empty((2, int(sizes.sum())), dtype=torch.float32, device=self.params[0].device)
+        flat = _held(torch.empty((2, int(sizes.sum())), dtype=torch.float32, device=self.params[0].device), stream)
         out = []
         for part in flat.unbind():
             out.append([t if p.dim() == 1 else t.view(p.shape) for t, p in zip(part.split(sizes.tolist()), self.params)])

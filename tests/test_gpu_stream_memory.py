@@ -41,3 +41,18 @@ def test_layer_for_a_few_tokens(dev):
     ref = ep.ep_moe_few_tokens(x, logits, k, *w)
     got = _behind(dev, lambda s: ep.ep_moe_few_tokens(x, logits, k, *w, stream=s))
     assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+def test_eight_bit_inputs_that_only_the_next_call_reads(dev):
+    M, N, K = 600, 264, 520
+    g = torch.Generator(device=dev).manual_seed(4)
+    x, w = torch.randn((M, K), generator=g, device=dev), torch.randn((2, N, K), generator=g, device=dev)
+    off = torch.tensor([0, 250, M], dtype=torch.int32, device=dev)
+
+    def product(stream):
+        xq, xs = ep.ep_quant_rows(x, stream=stream)
+        wq, ws = ep.ep_quant_blocks(w, stream=stream)
+        return ep.ep_grouped_matmul(xq, xs, wq, ws, off, stream=stream)
+
+    ref = product(None)
+    assert torch.equal(_behind(dev, product), ref)

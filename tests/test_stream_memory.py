@@ -62,3 +62,39 @@ def test_workspace_of_the_layer_for_a_few_tokens(told):
     ep.ep_moe_few_tokens(dev(3, 64, dtype=bf), dev(3, 4), 2, dev(4, 32, 64, dtype=bf), dev(4, 32, 64, dtype=bf),
                          dev(4, 64, 32, dtype=bf), out=out, ids=ids, weights=w, stream=Stream())
     assert len(made) == 1 and made <= lib.passed and made == kept
+
+
+def _calls():
+    bf, i32, u8, fp8 = torch.bfloat16, torch.int32, torch.uint8, torch.float8_e4m3fn
+    eight = lambda *s: dev(*s, dtype=u8).view(fp8)                       # noqa: E731
+    lay = ep.Layout(4, 2, 6, 2, 2, dev(64, dtype=i32), ep._CLayout())
+    off, s = dev(3, dtype=i32), Stream()
+    opt = ep.AdamW([dev(200)], bits=8)
+    for moments in (opt.exp_avg, opt.exp_avg_sq, opt.exp_avg_scale, opt.exp_avg_sq_scale):
+        moments[:] = [m.as_subclass(Dev) for m in moments]
+    return dict(
+        gate=(2, lambda: ep.ep_gate_topk(dev(5, 8), 2, stream=s)),
+        gate_backward=(1, lambda: ep.ep_gate_topk_backward(dev(5, 2, dtype=i32), dev(5, 2), dev(5, 2), 8, stream=s)),
+        quant_rows=(2, lambda: ep.ep_quant_rows(dev(5, 200), stream=s)),
+        swiglu=(2, lambda: ep.ep_swiglu_quant(dev(5, 200, dtype=bf), stream=s)),
+        quant_blocks=(2, lambda: ep.ep_quant_blocks(dev(2, 30, 200), stream=s)),
+        matmul=(1, lambda: ep.ep_grouped_matmul(eight(5, 128), dev(5, 4, dtype=u8), eight(2, 30, 128),
+                                                dev(2, 1, 1, dtype=u8), off, stream=s)),
+        wgrad=(1, lambda: ep.ep_grouped_wgrad(dev(5, 30, dtype=bf), dev(5, 20, dtype=bf), off, stream=s)),
+        wgrad_slots=(2, lambda: ep.ep_grouped_wgrad(dev(5, 30, dtype=bf), dev(5, 20, dtype=bf), dev(7, dtype=i32),
+                                                    layout=lay, stream=s)),
+        combine=(1, lambda: ep.ep_moe_combine(dev(5, 16, dtype=bf), dev(3, 2, dtype=i32), dev(3, 2), stream=s)),
+        few_tokens=(4, lambda: ep.ep_moe_few_tokens(dev(3, 64, dtype=bf), dev(3, 4), 2, dev(4, 32, 64, dtype=bf),
+                                                    dev(4, 32, 64, dtype=bf), dev(4, 64, 32, dtype=bf), stream=s)),
+        adamw_values=(1, lambda: opt.states(stream=s)))
+
+
+@pytest.mark.parametrize("name", ["gate", "gate_backward", "quant_rows", "swiglu", "quant_blocks", "matmul", "wgrad",
+                                  "wgrad_slots", "combine", "few_tokens", "adamw_values"])
+def test_outputs_of_the_layer_s_operators(told, name):
+    # a caller may drop them at once, as an 8-bit input that only the next call reads
+    lib, kept, made = told
+    count, call = _calls()[name]
+    made.clear()
+    call()
+    assert len(made) == count and made == kept
