@@ -147,6 +147,14 @@ def _stream(stream: Optional[torch.cuda.Stream]):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _held(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory that a call takes from torch's allocator, which hands it out for the current stream: where the call runs
+    on another one, it is not handed out again before that stream has passed the call."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 @dataclass
 class Layout:
     """Native placement + spare slots of one EP group, with its device tables."""
@@ -213,9 +221,11 @@ def ep_load_histogram(topk_ids: torch.Tensor, layout: Layout, load=None, ws=None
     """topk_ids int32 [P][N] -> (load int32 [P][E], ws, status uint32-as-int32 [P])."""
     P, N = _ids(topk_ids)
     dev = topk_ids.device
-    load = torch.empty((P, layout.num_experts), dtype=torch.int32, device=dev) if load is None else load
-    ws = workspace(topk_ids, layout) if ws is None else _ws(ws, N, P, layout)
-    status = torch.empty(P, dtype=torch.int32, device=dev) if status is None else status
+    if load is None:
+        load = _held(torch.empty((P, layout.num_experts), dtype=torch.int32, device=dev), stream)
+    ws = _held(workspace(topk_ids, layout), stream) if ws is None else _ws(ws, N, P, layout)
+    if status is None:
+        status = _held(torch.empty(P, dtype=torch.int32, device=dev), stream)
     _arg(load, torch.int32, (P, layout.num_experts), "load"); _arg(status, torch.int32, (P,), "status")
     rc = lib().ep_load_histogram(_ptr(topk_ids), N, P, layout.ref(), _ptr(load), _ptr(ws),
                                  ws.numel() * ws.element_size(), _ptr(status), _stream(stream))
@@ -246,7 +256,10 @@ def ep_plan_quota(load: torch.Tensor, layout: Layout, out: Optional[PlanOut] = N
     _dev(load, torch.int32, "load")
     P = load.shape[0]
     _arg(load, torch.int32, (P, layout.num_experts), "load")
-    out = alloc_plan(P, layout, load.device) if out is None else out
+    if out is None:
+        out = alloc_plan(P, layout, load.device)
+        for t in (out.phy2log, out.phy_quota, out.logcnt, out.log2phy, out.steps):
+            _held(t, stream)
     _arg(out.phy2log, torch.int32, (P, layout.num_phys), "phy2log")
     _plan_args(layout, P, out.phy_quota, out.log2phy, out.logcnt)
     _arg(out.steps, torch.int32, (P,), "steps")
@@ -264,7 +277,9 @@ def ep_reroute(topk_ids: torch.Tensor, layout: Layout, phy_quota: torch.Tensor, 
     P, N = _ids(topk_ids)
     _plan_args(layout, P, phy_quota, log2phy, logcnt)
     _ws(ws, N, P, layout)
-    phys_ids = torch.empty_like(topk_ids) if phys_ids is None else _arg(phys_ids, torch.int32, (P, N), "phys_ids")
+    if phys_ids is None:
+        phys_ids = _held(torch.empty_like(topk_ids), stream)
+    _arg(phys_ids, torch.int32, (P, N), "phys_ids")
     rc = lib().ep_reroute(_ptr(topk_ids), N, P, layout.ref(), _ptr(phy_quota), _ptr(log2phy),
                           _ptr(logcnt), _ptr(ws), ws.numel() * ws.element_size(), _ptr(phys_ids),
                           _stream(stream))
@@ -281,10 +296,10 @@ def ep_dispatch_layout(topk_ids: torch.Tensor, layout: Layout, phy_quota: torch.
     _ws(ws, N, P, layout)
     dev = topk_ids.device
     if slot_offsets is None:
-        slot_offsets = torch.empty((P, layout.num_phys + 1), dtype=torch.int32, device=dev)
+        slot_offsets = _held(torch.empty((P, layout.num_phys + 1), dtype=torch.int32, device=dev), stream)
     _arg(slot_offsets, torch.int32, (P, layout.num_phys + 1), "slot_offsets")
-    dispatch_pos = torch.empty_like(topk_ids) if dispatch_pos is None else dispatch_pos
-    dispatch_src = torch.empty_like(topk_ids) if dispatch_src is None else dispatch_src
+    dispatch_pos = _held(torch.empty_like(topk_ids), stream) if dispatch_pos is None else dispatch_pos
+    dispatch_src = _held(torch.empty_like(topk_ids), stream) if dispatch_src is None else dispatch_src
     _arg(dispatch_pos, torch.int32, (P, N), "dispatch_pos"); _arg(dispatch_src, torch.int32, (P, N), "dispatch_src")
     rc = lib().ep_dispatch_layout(_ptr(topk_ids), N, P, layout.ref(), _ptr(phy_quota), _ptr(log2phy),
                                   _ptr(logcnt), _ptr(ws), ws.numel() * ws.element_size(),
@@ -356,7 +371,7 @@ def ep_slot_fill(expert_weights: torch.Tensor, phy2log: torch.Tensor, layout: La
     if slot_buf.numel() * slot_buf.element_size() < layout.num_spare * bpe:
         raise EPBalanceError("slot_buf is smaller than S * bytes_per_expert")
     if ws is None and use_ws:
-        ws = slot_fill_workspace(layout, expert_weights.device)
+        ws = _held(slot_fill_workspace(layout, expert_weights.device), stream)
     if ws is not None and not (ws.is_cuda and ws.is_contiguous()):
         raise EPBalanceError("ws must be a contiguous device tensor")
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
@@ -374,10 +389,12 @@ def ep_balance_stats(load: torch.Tensor, phy_quota: torch.Tensor, layout: Layout
     _arg(load, torch.int32, (P, layout.num_experts), "load")
     _arg(phy_quota, torch.int32, (P, layout.num_phys), "phy_quota")
     dev = load.device
-    stats = torch.empty((P, 4), dtype=torch.int64, device=dev) if stats is None else stats
-    imbalance = torch.empty((P, 2), dtype=torch.float64, device=dev) if imbalance is None else imbalance
+    if stats is None:
+        stats = _held(torch.empty((P, 4), dtype=torch.int64, device=dev), stream)
+    if imbalance is None:
+        imbalance = _held(torch.empty((P, 2), dtype=torch.float64, device=dev), stream)
     if rank_load is None and want_rank_load:
-        rank_load = torch.empty((P, 2, layout.num_ranks), dtype=torch.int32, device=dev)
+        rank_load = _held(torch.empty((P, 2, layout.num_ranks), dtype=torch.int32, device=dev), stream)
     _arg(stats, torch.int64, (P, 4), "stats"); _arg(imbalance, torch.float64, (P, 2), "imbalance")
     if rank_load is not None:
         _arg(rank_load, torch.int32, (P, 2, layout.num_ranks), "rank_load")

@@ -11,7 +11,7 @@ from typing import List, Optional, Sequence
 import numpy as np
 import torch
 
-from . import (EPBalanceError, Layout, _check, _CLayout, ep_dispatch_layout, ep_load_histogram, ep_plan_quota,
+from . import (EPBalanceError, Layout, _check, _CLayout, _held, ep_dispatch_layout, ep_load_histogram, ep_plan_quota,
                ep_slot_fill, lib)
 from . import _arg as _arg_or_raise
 
@@ -97,14 +97,6 @@ def _ptr(t: torch.Tensor) -> int:
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     """The given stream, or torch's current one, as a pointer."""
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
-
-
-def _held(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """Memory that a call takes from torch's allocator, which hands it out for the current stream: where the call runs
-    on another one, it is not handed out again before that stream has passed the call."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 def _rows(t: torch.Tensor, dtypes, name: str) -> int:

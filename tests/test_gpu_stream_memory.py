@@ -56,3 +56,26 @@ def test_eight_bit_inputs_that_only_the_next_call_reads(dev):
 
     ref = product(None)
     assert torch.equal(_behind(dev, product), ref)
+
+
+def test_balancing_path_and_slot_fill(dev):
+    lay = ep.Layout.create(16, [2] * 8, list(range(16)), [1] * 8, device=dev)
+    g = torch.Generator(device=dev).manual_seed(5)
+    ids = (torch.rand((1, 4096), generator=g, device=dev) ** 3 * 16).to(torch.int32)
+    rows = torch.randint(0, 255, (16, 1 << 14), generator=g, device=dev, dtype=torch.uint8)
+
+    def path(stream):
+        load, ws, status = ep.ep_load_histogram(ids, lay, stream=stream)
+        plan = ep.ep_plan_quota(load, lay, status=status, stream=stream)
+        slots = torch.zeros((8, 1 << 14), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            slots.record_stream(stream)
+            stream.wait_stream(torch.cuda.current_stream())
+        ep.ep_slot_fill(rows, plan.phy2log[0], lay, slots, stream=stream)
+        return ep.ep_dispatch_layout(ids, lay, plan.phy_quota, plan.log2phy, plan.logcnt, ws, stream=stream)[1:], slots
+
+    (pos, src), slots = path(None)
+    assert (slots != 0).any()
+    (pos2, src2), slots2 = _behind(dev, path)
+    assert torch.equal(pos, pos2) and torch.equal(src, src2)
+    assert torch.equal(slots, slots2)

@@ -47,6 +47,7 @@ def told(monkeypatch):
         made.add(t.data_ptr())
         return t
 
+    monkeypatch.setattr(torch, "empty_like", lambda t: counted(t.shape, dtype=t.dtype))
     monkeypatch.setattr(M, "lib", lambda: lib)
     monkeypatch.setattr(ep, "lib", lambda: lib)
     monkeypatch.setattr(torch, "empty", counted)
@@ -96,5 +97,24 @@ def test_outputs_of_the_layer_s_operators(told, name):
     lib, kept, made = told
     count, call = _calls()[name]
     made.clear()
+    call()
+    assert len(made) == count and made == kept
+
+
+@pytest.mark.parametrize("name", ["histogram", "plan", "reroute", "dispatch", "stats", "slot_fill", "path"])
+def test_memory_of_the_balancing_path(told, name):
+    lib, kept, made = told
+    i32 = torch.int32
+    lay, s = ep.Layout(4, 2, 6, 2, 2, dev(64, dtype=i32), ep._CLayout()), Stream()
+    ids, load, ws = dev(1, 20, dtype=i32), dev(1, 4, dtype=i32), dev(4096, dtype=torch.uint8)
+    plan = (dev(1, 6, dtype=i32), dev(1, 4, 2, dtype=i32), dev(1, 4, dtype=i32))
+    count, call = dict(
+        histogram=(3, lambda: ep.ep_load_histogram(ids, lay, stream=s)),
+        plan=(5, lambda: ep.ep_plan_quota(load, lay, stream=s)),
+        reroute=(1, lambda: ep.ep_reroute(ids, lay, *plan, ws, stream=s)),
+        dispatch=(3, lambda: ep.ep_dispatch_layout(ids, lay, *plan, ws, stream=s)),
+        stats=(3, lambda: ep.ep_balance_stats(load, plan[0], lay, stream=s)),
+        slot_fill=(1, lambda: ep.ep_slot_fill(dev(4, 32), dev(6, dtype=i32), lay, dev(2, 32), stream=s)),
+        path=(12, lambda: ep.run_path(ids, lay, stream=s)))[name]
     call()
     assert len(made) == count and made == kept
