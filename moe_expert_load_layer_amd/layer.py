@@ -489,6 +489,8 @@ class AdamW:
             columns.append((1, grads, grads[0].dtype if grads else torch.float32, "grads"))
             if self.copies is not None:
                 columns.append((6, self.copies, torch.bfloat16, "copies"))
+            else:
+                words[:, 6] = 0
         if eight:
             lengths = self._scales
             columns += [(4, self.exp_avg_scale, torch.uint8, "exp_avg_scale"),
