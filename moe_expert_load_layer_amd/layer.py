@@ -472,16 +472,20 @@ class AdamW:
             self.exp_avg_scale, self.exp_avg_sq_scale = (
                 [torch.ones((p.numel() + 127) // 128, dtype=torch.uint8, device=p.device) for p in self.params]
                 for _ in range(2))
-        self._scales = [((p.numel() + 127) // 128,) for p in self.params]
-        # the library's descriptors, one a row, as the 8 words of ep_adamw_tensor_t
-        self._words = np.zeros((len(self.params), 8), dtype=np.int64)
-        self._words[:, 7] = [p.numel() for p in self.params]
+        self._sizes: Optional[List[int]] = None
 
     def _tensors(self, grads: Optional[Sequence[torch.Tensor]] = None) -> int:
         """The descriptors' address; the lists above may have been given other tensors (a checkpoint's), so all are
         looked at."""
         state = torch.float32 if self.bits == 32 else torch.uint8
-        params, words, eight = self.params, self._words, self.bits == 8
+        params, eight = self.params, self.bits == 8
+        sizes = [p.numel() for p in params]
+        if sizes != self._sizes:
+            self._sizes, self._scales = sizes, [((n + 127) // 128,) for n in sizes]
+            # the library's descriptors, one a row, as the 8 words of ep_adamw_tensor_t
+            self._words = np.zeros((len(params), 8), dtype=np.int64)
+            self._words[:, 7] = sizes
+        words = self._words
         shapes = [p.shape for p in params]
         columns = [(0, params, torch.float32, "params"), (2, self.exp_avg, state, "exp_avg"),
                    (3, self.exp_avg_sq, state, "exp_avg_sq")]
@@ -527,6 +531,7 @@ class AdamW:
         n = len(self.params)
         if n == 0:
             return [], []
+        tensors = self._tensors()
         # the values of all tensors lie one after the other in one piece of memory
         sizes = self._words[:, 7]
         flat = _held(torch.empty((2, int(sizes.sum())), dtype=torch.float32, device=self.params[0].device), stream)
@@ -535,6 +540,6 @@ class AdamW:
             out.append([t if p.dim() == 1 else t.view(p.shape) for t, p in zip(part.split(sizes.tolist()), self.params)])
         mp = flat.data_ptr() + 4 * (np.cumsum(sizes) - sizes)
         vp = mp + 4 * flat.shape[1]
-        _check(lib().ep_adamw_values(self._tensors(), n, mp.ctypes.data, vp.ctypes.data, _stream(stream)),
+        _check(lib().ep_adamw_values(tensors, n, mp.ctypes.data, vp.ctypes.data, _stream(stream)),
                "ep_adamw_values")
         return out[0], out[1]
