@@ -565,7 +565,9 @@ int ep_moe_few_tokens(const void *x, int64_t x_stride, int32_t num_tokens, const
  * [ceil(numel / 128)]; m as sign, 4 bits of exponent, 3 of mantissa, v as 5 bits
  * of exponent, 3 of mantissa (never 0 for v > 0), rounded stochastically from a
  * hash of (seed, step, index of the tensor, element), so that a run repeats bit
- * for bit.  Fresh states are all 0 with scale bytes 1.
+ * for bit.  Fresh states are all 0 with scale bytes 1.  The codes hold no infinity
+ * and no NaN: an infinite or NaN gradient shows in its parameter, which is NaN from
+ * then on; its moments become 0 and leave the rest of their block alone.
  * The array of descriptors is host memory and read at enqueue time.
  */
 typedef struct ep_adamw_tensor {

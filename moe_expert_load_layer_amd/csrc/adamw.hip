@@ -217,6 +217,9 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Args A, const Hyp
         float am = 0.0f, av = 0.0f;
 #pragma unroll
         for (int k = 0; k < kUnit; k++) {
+            // an infinite or NaN gradient: the parameter is lost, and its moments must
+            // not set the scale of the block's others
+            if (!(fabsf(m[k]) < INFINITY)) m[k] = v[k] = 0.0f;
             am = fmaxf(am, fabsf(m[k]));
             av = fmaxf(av, v[k]);
         }
