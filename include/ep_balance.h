@@ -428,8 +428,8 @@ int ep_gate_topk_backward(const int32_t *ids, const float *weights, const float 
 /*
  * 8-bit floating point with a scale for each block of 128: values are OCP e4m3
  * bytes, and a block's scale is the byte c, standing for 2^(c - 127), the
- * smallest power of two that brings the block's largest magnitude to 448 at
- * most.  Rounding is to nearest, ties to even; NaN and infinities become NaN.
+ * smallest power of two that brings the block's largest finite magnitude to 448
+ * at most.  Rounding is to nearest, ties to even; NaN and infinities become NaN.
  *
  * ep_quant_rows: blocks of 128 columns of one row, for activations.
  *   x      device [rows][stride] fp32 or bf16

@@ -39,3 +39,48 @@ def test_moments_of_a_block(dev, value, dtype):
     assert torch.isnan(p[lost]).all()
     for a, b in ((p, rp), (m, rm), (v, rv)):
         assert torch.equal(a[~lost], b[~lost])
+
+
+def _apart(dev, dtype, bad):
+    """A matrix [200][300] and the same with `bad` in three places."""
+    g = torch.Generator(device=dev).manual_seed(2)
+    w = torch.randn((200, 300), generator=g, device=dev).to(dtype)
+    lost = torch.zeros((200, 300), dtype=torch.bool, device=dev)
+    lost[5, 7] = lost[130, 131] = lost[199, 299] = True
+    return torch.where(lost, torch.zeros_like(w), w), torch.where(lost, torch.full_like(w, bad), w), lost
+
+
+def _only_lost_differ(a, b, lost):
+    """8-bit values and scale bytes, the second with NaN where `lost`."""
+    (q, s), (qb, sb) = a, b
+    assert torch.equal(s, sb)
+    q, qb = q.view(torch.uint8)[..., :lost.shape[-1]], qb.view(torch.uint8)[..., :lost.shape[-1]]
+    assert torch.equal(q[~lost], qb[~lost]) and ((qb[lost] & 127) == 127).all()
+
+
+@pytest.mark.parametrize("bad", [INF, -INF, NAN])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_eight_bit_blocks(dev, bad, dtype):
+    w, wb, lost = _apart(dev, dtype, bad)
+    _only_lost_differ(ep.ep_quant_rows(w), ep.ep_quant_rows(wb), lost)
+    _only_lost_differ(ep.ep_quant_blocks(w[None]), ep.ep_quant_blocks(wb[None]), lost[None])
+    _only_lost_differ(ep.ep_quant_blocks(w[None], transpose=True), ep.ep_quant_blocks(wb[None], transpose=True),
+                      lost.t()[None])
+
+
+@pytest.mark.parametrize("bad", [INF, NAN])
+def test_eight_bit_blocks_of_silu(dev, bad):
+    u, ub, lost = _apart(dev, torch.bfloat16, bad)
+    gate = torch.full_like(u, 1.5)
+    _only_lost_differ(ep.ep_swiglu_quant(torch.cat([gate, u], dim=1)), ep.ep_swiglu_quant(torch.cat([gate, ub], dim=1)),
+                      lost)
+
+
+def test_product_with_an_infinite_weight(dev):
+    # one infinite weight makes its own column of y infinite or NaN, and no other one smaller
+    w, wb, lost = _apart(dev, torch.bfloat16, INF)
+    g = torch.Generator(device=dev).manual_seed(3)
+    xq, xs = ep.ep_quant_rows(torch.randn((40, 300), generator=g, device=dev))
+    y, yb = (ep.ep_grouped_matmul(xq, xs, *ep.ep_quant_blocks(m[None])) for m in (w, wb))
+    column = lost.any(dim=1)
+    assert torch.isnan(yb[:, column]).all() and torch.equal(y[:, ~column], yb[:, ~column])
