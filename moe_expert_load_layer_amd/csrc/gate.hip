@@ -60,7 +60,7 @@ template <bool kBf16>
 __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const int32_t *__restrict__ ids,
                                                                  const float *__restrict__ weights,
                                                                  const float *__restrict__ grad, int64_t T, int E,
-                                                                 int k, float inv_scale, void *__restrict__ out) {
+                                                                 int k, float scale, void *__restrict__ out) {
     constexpr int kTok = kWave / kGateLanes, kWidth = kBf16 ? 2 : 4, kPer = 16 / kWidth;
     extern __shared__ u32x4 lds[];  // [waves][4 rows of E, up to 16 bytes]
     const int l = lane_id(), wave = threadIdx.x / kWave, lane = l % kGateLanes;
@@ -73,7 +73,9 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const int32_t *
     const float w = use ? weights[t * k + lane] : 0.0f;
     const float g = use ? grad[t * k + lane] : 0.0f;
     for (int i = l; i < words; i += kWave) mine[i] = u32x4{0, 0, 0, 0};
-    const float mean = row_sum_f32(w * g) * inv_scale;
+    const float sum = row_sum_f32(w * g);
+    // divided, since the smallest scales have no finite inverse
+    const float mean = scale != 0.0f ? sum / scale : 0.0f;
     wave_lds_fence();
     if (use) {
         const float d = w * (g - mean);
@@ -128,15 +130,14 @@ extern "C" int ep_gate_topk_backward(const int32_t *ids, const float *weights, c
     if (!ids || !weights || !grad_weights || !grad_logits || !is_aligned(ids, 4) || !is_aligned(weights, 4) ||
         !is_aligned(grad_weights, 4) || !is_aligned(grad_logits, bf16 ? 2 : 4))
         return EP_ERR_INVALID_ARG;
-    const float inv = gate->scale != 0.0f ? 1.0f / gate->scale : 0.0f;
     const dim3 grid((uint32_t)ceil_div(num_tokens, kTokens));
     const size_t lds = (size_t)(kThreads / kWave) * ceil_div(4 * (int64_t)gate->num_experts * (bf16 ? 2 : 4), 16) * 16;
     const hipStream_t s = to_stream(stream);
     if (bf16)
         gate_backward_kernel<true><<<grid, kThreads, lds, s>>>(ids, weights, grad_weights, num_tokens,
-                                                               gate->num_experts, gate->top_k, inv, grad_logits);
+                                                               gate->num_experts, gate->top_k, gate->scale, grad_logits);
     else
         gate_backward_kernel<false><<<grid, kThreads, lds, s>>>(ids, weights, grad_weights, num_tokens,
-                                                                gate->num_experts, gate->top_k, inv, grad_logits);
+                                                                gate->num_experts, gate->top_k, gate->scale, grad_logits);
     return rc_of(hipGetLastError());
 }

@@ -84,3 +84,21 @@ def test_product_with_an_infinite_weight(dev):
     y, yb = (ep.ep_grouped_matmul(xq, xs, *ep.ep_quant_blocks(m[None])) for m in (w, wb))
     column = lost.any(dim=1)
     assert torch.isnan(yb[:, column]).all() and torch.equal(y[:, ~column], yb[:, ~column])
+
+
+@pytest.mark.parametrize("scale", [1e-39, -3e-39, 2.0 ** -128, 1e-30])
+def test_gate_gradient_with_the_smallest_scales(dev, scale):
+    # 1 / scale is not finite below 2^-128; w, w g and their sum are whole multiples of 2^-149, rounded once or twice
+    # each: (k + 3) 2^-149 for the mean's numerator, which dividing by the scale and multiplying by w <= |scale| keeps
+    T, E, k = 9, 16, 4
+    g = torch.Generator(device=dev).manual_seed(6)
+    logits, grad = torch.randn((T, E), generator=g, device=dev), torch.randn((T, k), generator=g, device=dev)
+    ids, w = ep.ep_gate_topk(logits, k, scale=scale)
+    got = ep.ep_gate_topk_backward(ids, w, grad, E, scale=scale)
+    assert torch.isfinite(got).all()
+    s, a = float(torch.tensor(scale, dtype=torch.float32)), w.double()
+    d = a * (grad.double() - (a * grad.double()).sum(dim=1, keepdim=True) / s)
+    ref = torch.zeros((T, E), dtype=torch.float64, device=dev).scatter_(1, ids.long(), d)
+    size = a.abs() * (grad.double().abs() + (a * grad.double()).abs().sum(dim=1, keepdim=True) / abs(s))
+    bound = torch.zeros_like(ref).scatter_(1, ids.long(), (k + 6) * 2.0 ** -24 * size) + (k + 6) * 2.0 ** -149
+    assert ((got.double() - ref).abs() <= bound).all()
