@@ -421,6 +421,9 @@ def run_layer(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layout, exp
     x bf16 [tokens][H], logits [tokens][E] (rank by rank, the same number of tokens each); experts: the native
     experts' rows, slots: the spare slots' (filled here).  Returns a dict: out bf16 [tokens][H], ids, weights, plan,
     offsets, pos, src, h (the 8-bit input of the second product and its scales)."""
+    if x.dim() != 2 or logits.dim() != 2 or x.shape[0] != logits.shape[0]:
+        raise EPBalanceError(f"x [tokens][hidden] and logits [tokens][experts] must have the same tokens, got "
+                             f"{tuple(x.shape)} and {tuple(logits.shape)}")
     ids, weights = ep_gate_topk(logits, k, bias, num_groups, topk_groups, scale)
     pairs = ids.view(1, -1)
     load, ws, status = ep_load_histogram(pairs, layout)
