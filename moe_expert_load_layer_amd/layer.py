@@ -475,23 +475,27 @@ class AdamW:
             self.exp_avg_scale, self.exp_avg_sq_scale = (
                 [torch.ones((p.numel() + 127) // 128, dtype=torch.uint8, device=p.device) for p in self.params]
                 for _ in range(2))
-        self._sizes: Optional[List[int]] = None
+        self._shapes: Optional[List[torch.Size]] = None
 
     def _tensors(self, grads: Optional[Sequence[torch.Tensor]] = None) -> int:
         """The descriptors' address; the lists above may have been given other tensors (a checkpoint's), so all are
         looked at."""
         state = torch.float32 if self.bits == 32 else torch.uint8
         params, eight = self.params, self.bits == 8
-        sizes = [p.numel() for p in params]
-        if sizes != self._sizes:
-            self._sizes, self._scales = sizes, [((n + 127) // 128,) for n in sizes]
+        shapes = [p.shape for p in params]
+        if shapes != self._shapes:
+            sizes = [p.numel() for p in params]
+            self._shapes, self._scales = shapes, [((n + 127) // 128,) for n in sizes]
             # the library's descriptors, one a row, as the 8 words of ep_adamw_tensor_t
             self._words = np.zeros((len(params), 8), dtype=np.int64)
             self._words[:, 7] = sizes
         words = self._words
-        shapes = [p.shape for p in params]
-        columns = [(0, params, torch.float32, "params"), (2, self.exp_avg, state, "exp_avg"),
-                   (3, self.exp_avg_sq, state, "exp_avg_sq")]
+        if not all([p.dtype is torch.float32 and p.is_cuda and p.is_contiguous() for p in params]):
+            for i, p in enumerate(params):
+                _arg_or_raise(p, torch.float32, p.shape, f"params[{i}]")
+        if params:
+            words[:, 0] = [p.data_ptr() for p in params]
+        columns = [(2, self.exp_avg, state, "exp_avg"), (3, self.exp_avg_sq, state, "exp_avg_sq")]
         if grads is not None:
             columns.append((1, grads, grads[0].dtype if grads else torch.float32, "grads"))
             if self.copies is not None:
