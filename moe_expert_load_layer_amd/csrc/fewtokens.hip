@@ -414,7 +414,7 @@ __global__ __launch_bounds__(kThreads) void down_kernel(const FewArgs A) {
     __shared__ float weights[kMaxPairs];
     __shared__ uint8_t scales[kFp8 ? kScaleUnits : 1];
     __shared__ int arrived;
-    extern __shared__ float part[];  // [kWaves][T][16]
+    extern __shared__ __align__(16) float part[];  // [kWaves][T][16], read four at a time
     static_assert(sizeof(Scratch) <= sizeof(stages), "the scratch fits the stages");
     Scratch *W = reinterpret_cast<Scratch *>(stages);
     for (int p = threadIdx.x; p < A.T * A.k; p += kThreads) {
