@@ -532,8 +532,10 @@ int ep_moe_combine(const void *y, int64_t rows, const int32_t *pos, const float 
  * A whole mixture-of-experts layer for up to EP_MAX_FEW_TOKENS tokens:
  *   ids, w  as ep_gate_topk
  *   out_t = sum_j w_tj down_e (silu(gate_e x_t) * (up_e x_t)),  e = ids_tj >= 0
- * summed in fp32 and rounded to bf16 once.  Every distinct expert's weights are
- * read once.
+ * summed in fp32 and rounded to bf16 once; between the products h is held as the
+ * sum of two bf16, 16 bits of mantissa.  With up to 8 tokens every distinct expert's
+ * weights are read once; with more, gate and up once for every 32 of its tokens
+ * and down once for every 16.  The experts are the native ones: there is no layout.
  *   x        device bf16 [T][x_stride], 16-byte aligned, x_stride a multiple of 8
  *   logits   as for ep_gate_topk
  *   experts  bf16 matrices gate, up [E][inter][hidden], down [E][hidden][inter],

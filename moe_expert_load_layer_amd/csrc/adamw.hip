@@ -21,9 +21,9 @@
 // Bound: HBM.  28 bytes an element with fp32 moments and gradients, 16 with
 // 8-bit moments.  A lane takes 8 consecutive elements (32-byte accesses, 16
 // lanes = one scale block = one DPP row, whose maximum takes 4 DPP steps).
-// Measured: 8-bit moments 364 us for 113 million elements (5.0 TB/s), their
-// values 235 us (4.8); fp32 moments, bf16 gradients and a bf16 copy 510 us for 94
-// million (5.2).  12 tensors of 5003 elements take one launch of 5.3 us.
+// Measured: 8-bit moments 341 us for 113 million elements (5.3 TB/s), their
+// values 231 us (4.9); fp32 moments, bf16 gradients and a bf16 copy 507 us for 94
+// million (5.2).  12 tensors of 5003 elements take one launch of 4.9 us.
 #include <math.h>
 
 #include "layer.h"

@@ -4,13 +4,14 @@
 //
 // With more than 32 tokens the gate is a launch of its own before them.
 //
-// Bound: HBM.  Every distinct expert's three matrices are read once, which is
-// all but a fraction of a percent of the bytes.  (With more than 8 tokens, gate
+// Bound: HBM.  With up to 8 tokens every distinct expert's three matrices are read
+// once, which is all but a fraction of a percent of the bytes.  With more, gate
 // and up are read once for every 32 tokens of an expert and down once for every
-// 16: more columns would leave LDS for fewer workgroups.)
-// Measured, up and down: 1 token, 8 of 128 experts, 4096 x 1536 in bf16 44 + 22 us
-// (302 MB, 4.6 TB/s); 7 tokens, 7168 x 2048 in 8 bits 173 + 93 us (1.40 GB, 5.3);
-// 61 tokens, 160 experts, 5120 x 1536 in bf16 5 + 509 + 275 us (4.34 GB, 5.5).
+// 16 (more columns would leave LDS for fewer workgroups): 10 % more bytes of down
+// at 61 tokens on 160 experts, four times its bytes where all 64 tokens agree.
+// Measured, up and down: 1 token, 8 of 128 experts, 4096 x 1536 in bf16 43 + 22 us
+// (302 MB, 4.6 TB/s); 7 tokens, 7168 x 2048 in 8 bits 175 + 91 us (1.40 GB, 5.3);
+// 61 tokens, 160 experts, 5120 x 1536 in bf16 5 + 508 + 282 us (4.34 GB, 5.5).
 //
 // Both kernels stream: a workgroup takes 64 weight rows of an expert and walks
 // them in windows of 128 bytes a row, together with the same window of the

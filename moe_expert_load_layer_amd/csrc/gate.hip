@@ -3,10 +3,10 @@
 // 16 lanes take a token (gate.h), a wave four, a workgroup 16.  Forward reads
 // the logits once and is bound by the instructions of the selection; backward
 // writes the dense gradient rows, assembled in LDS, and is bound by HBM.
-// Measured for 131071 tokens x 384 experts in bf16, k = 8: forward 31 us (3.5
-// TB/s; k rounds of a maximum over the row take 66), backward 17 us
-// (6.8 TB/s); 64 tokens x 256 experts in fp32 7 us, most of it a launch and the
-// loads' latency.
+// Measured for 131071 tokens x 384 experts in bf16, k = 8: forward 36 us (3.0
+// TB/s; 28 where the logits are in the last-level cache, and k rounds of a maximum
+// over the row take 66), backward 18 us (6.3 TB/s); 64 tokens x 256 experts in fp32
+// 7 us, most of it a launch and the loads' latency.
 #include "gate.h"
 
 namespace ep {

@@ -6,9 +6,9 @@
 // exact, so a value is rounded once, to nearest with ties to even.  NaN and
 // infinities become NaN, and leave their block's scale alone.  All four kernels are one pass over the data, bound by HBM.
 // Measured, bytes read and written once (a 2 GiB copy reaches 4.95 TB/s):
-//   rows of bf16      65536 x 4096      147 us  5.5 TB/s   (8192 x 4096: 24 us, 4.2)
-//   rows of fp32      32768 x 4096      114 us  5.9 TB/s
-//   silu(g) u         65536 x 2 x 2048  125 us  5.4 TB/s
+//   rows of bf16      65536 x 4096      139 us  5.8 TB/s   (8192 x 4096: 22 us, 4.6)
+//   rows of fp32      32768 x 4096      115 us  5.8 TB/s
+//   silu(g) u         65536 x 2 x 2048  113 us  6.0 TB/s
 //   blocks of bf16    16 x 8192 x 4096  288 us  5.6 TB/s, transposed or not
 //   combine           8192 x 8 x 4096   126 us  4.8 TB/s
 //

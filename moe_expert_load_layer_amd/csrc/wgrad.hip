@@ -12,8 +12,8 @@
 // rows of 32 bytes for 16 lanes; the 16-byte chunks of an LDS row are exchanged
 // by the row's bits 0 and 1, so that the rows read together meet different banks.
 //
-// Bound: the matrix pipes.  16381 rows in 3 groups, N = 2048, K = 4096: 316 us,
-// 870 TFLOP/s, against 1190 of a large library product in bf16.  Tiles of
+// Bound: the matrix pipes.  16381 rows in 3 groups, N = 2048, K = 4096: 272 us,
+// 1010 TFLOP/s, against 1190 of a large library product in bf16.  Tiles of
 // 256 x 128 by 4 waves of 128 x 64 leave LDS for two workgroups a CU: while one
 // waits at its barrier or stores its tile, the other multiplies.  One workgroup
 // of 256 x 256 a CU took 13 us more.
@@ -291,8 +291,9 @@ extern "C" int ep_grouped_wgrad(const ep_grouped_wgrad_t *p, ep_stream_t stream)
     A.out_stride = p->out_stride;
     A.slot_out_stride = p->slot_out_stride;
     // Straight into LDS where whole chunks of 8 columns are inside or outside and every
-    // row starts on 16 bytes; else through registers: 12001 rows in 5 groups, 2047 x 3001
-    // 378 us (390 TFLOP/s against 870).
+    // row starts on 16 bytes; else through registers, with one step's loads in flight
+    // instead of two: 12001 rows in 5 groups, 2047 x 3001 330 us, 450 TFLOP/s, less than
+    // half of the other form's rate.
     A.vec = p->n % 8 == 0 && p->k % 8 == 0 && is_aligned(p->dy, 16) && is_aligned(p->x, 16) && p->dy_stride % 8 == 0 &&
             p->x_stride % 8 == 0;
     return rc_of(launch(A, to_stream(stream)));

@@ -391,7 +391,10 @@ def ep_moe_few_tokens(x: torch.Tensor, logits: torch.Tensor, k: int, gate: torch
 
 class ExpertRows:
     """8-bit weights of a layer's experts, one packed row of bytes each: gate above up [2 I][H], down [H][I], then
-    their scales.  A row is what ep_slot_fill copies, so a buffer of spare slots has the same views."""
+    their scales.  A row is what ep_slot_fill copies, so a buffer of spare slots has the same views.
+
+    ep_moe_few_tokens takes gate and up apart: gate_up and gate_up_scale split into halves where inter is a multiple
+    of 128.  Elsewhere one scale byte covers rows of both, and the halves need an ep_quant_blocks of their own."""
 
     def __init__(self, count: int, hidden: int, inter: int, device):
         self.hidden, self.inter = hidden, inter
