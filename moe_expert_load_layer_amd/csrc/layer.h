@@ -38,6 +38,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // 2^(c - 127) for c in 1..254
 __device__ __forceinline__ float pow2_of(int c) { return __builtin_bit_cast(float, (uint32_t)c << 23); }
 
+// The scale byte of a block in 8 bits whose largest finite magnitude is amax: the
+// smallest c with amax <= 448 * 2^(c - 127)
+__device__ __forceinline__ int fp8_scale_code(float amax) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, amax);
+    const int c = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);
+    return min(max(c, 1), 254);
+}
+
 // One DPP step: the value of the lane that `ctrl` names, in the row of 16
 template <int ctrl>
 __device__ __forceinline__ float dpp_f32(float v) {

@@ -23,12 +23,6 @@ constexpr int kThreads = 256;
 constexpr int kUnitLanes = kScaleBlock / 8;
 constexpr int kUnits = kThreads / kUnitLanes;  // blocks of a workgroup
 
-__device__ __forceinline__ int fp8_scale_code(float amax) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, amax);
-    const int c = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);
-    return min(max(c, 1), 254);
-}
-
 // x / 2^(c - 127) as 8 bytes.  The conversion turns infinities into NaN.
 __device__ __forceinline__ u32x2 to_fp8(const float (&x)[8], int c) {
     const float inv = pow2_of(254 - c);

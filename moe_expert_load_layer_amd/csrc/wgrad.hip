@@ -22,15 +22,10 @@
 // and stores 16 bytes.  Rows past the group's end and columns past the matrix
 // are fetched from a block of zeros, so that neighbours' values (which may be
 // infinite) never enter.
-#include "groups.h"
+#include "columns.h"
 
 namespace ep {
 namespace {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-__device__ __align__(16) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
 struct WgradArgs {
     const uint16_t *dy, *x;
@@ -49,26 +44,6 @@ constexpr int kTileK = 256, kTileN = 128;  // columns of x and of dy
 constexpr int kWaveK = 128, kWaveN = 64;
 constexpr int kWavesK = kTileK / kWaveK, kWaves = kWavesK * (kTileN / kWaveN), kThreads = kWaves * kWave;
 constexpr int kStages = 3;
-
-// the 16-byte chunk of an LDS row that holds chunk c of the matrix row
-__device__ __forceinline__ int swizzle(int row, int c) { return c ^ ((row & 3) << 2); }
-
-// rows t .. t + 7 (this lane's half of 16) of column c0 + l % 32, as 8 bf16
-template <int kCols>
-__device__ __forceinline__ bf16x8 read_columns(const uint16_t *tile, int t0, int c0) {
-    const int l = lane_id(), i = l & 15, c = c0 + ((l >> 4) & 1) * 16 + (i & 3) * 4;
-    union {
-        s16x4 h[2];
-        bf16x8 v;
-    } u;
-#pragma unroll
-    for (int p = 0; p < 2; p++) {
-        const int t = t0 + (l >> 5) * 8 + p * 4 + (i >> 2);
-        const uint16_t *a = tile + t * kCols + swizzle(t, c / 8) * 8 + c % 8;
-        u.h[p] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)a);
-    }
-    return u.v;
-}
 
 // The loads of one operand: a wave's 1 KiB loads hold whole LDS rows of kCols.
 template <int kCols, bool kVec>
