@@ -520,6 +520,122 @@ typedef struct ep_grouped_wgrad {
 int ep_grouped_wgrad(const ep_grouped_wgrad_t *p, ep_stream_t stream);
 
 /*
+ * The same from rows of x that are held in 8 bits, as ep_quant_rows or
+ * ep_grouped_swiglu wrote them, each operand gathered or not:
+ *   out_g[n][k] = sum over the rows i of group g of dy[d(i)][n] x[r(i)][k]
+ * fp32, every element written.  d(i) = dy_places[i] / rows_div, or i without dy_places;
+ * r(i) likewise with x_places.  Given both, they are one and the same list.  A row whose
+ * place is negative or too large adds nothing.
+ *   dy       device bf16 [dy_rows][dy_stride]; dy_rows >= m without dy_places
+ *   x, x_scale  rows of k values in 8 bits, x_rows of them; x_rows >= m without x_places
+ *   dy_places, x_places  device int32 [m] or NULL
+ */
+typedef struct ep_grouped_wgrad_mixed {
+    const void *dy;
+    int64_t dy_rows, dy_stride;
+    const void *x;
+    const uint8_t *x_scale;
+    int64_t x_rows;
+    const int32_t *dy_places, *x_places;
+    int32_t rows_div;
+    int32_t groups;
+    const int32_t *offsets;
+    int64_t m, n, k;
+    const ep_layout_t *layout;
+    float *out, *slot_out;
+    int64_t out_stride, slot_out_stride;
+} ep_grouped_wgrad_mixed_t;
+int ep_grouped_wgrad_mixed(const ep_grouped_wgrad_mixed_t *p, ep_stream_t stream);
+
+/*
+ * The gated feed-forward block over the same groups of rows.  For output row i of
+ * group g with the input row r(i), as in ep_grouped_matmul:
+ *   a = gate_g x[r(i)],  b = up_g x[r(i)],  h[i] = w_i silu(a) b   (fp32, then 8 bits)
+ * with w_i = weights[rows[i]] (rows NULL: weights[i]; weights NULL: 1).  With the
+ * combine's weights here, the combine after the product of h with the matrices
+ * back takes weights of 1.
+ *   gate, up, slot_gate, slot_up   [groups][inter][k], as ep_quant_blocks writes each
+ *   weights  device float [weights_count] or NULL; a row of a pair past them has no
+ *            input (rows NULL: weights_count >= m)
+ *   h, h_scale  rows of inter values in 8 bits (the layout of ep_quant_rows), every
+ *            byte written; rows without an input (rows[i] negative or too large) and rows
+ *            from offsets[groups] on are rows of zeros
+ *   keep     NULL, or what ep_grouped_swiglu_backward needs of a and b, keep_dtype:
+ *            EP_DTYPE_BF16  bf16 [m][2 * inter], a and then b
+ *            EP_DTYPE_FP8   in 8 bits: bytes [m][2 * I], I = inter up to a multiple of
+ *                           128: a, zeros, b, zeros, and keep_scale with
+ *                           ep_scale_stride(2 * I) bytes a row
+ *            rows without an input and past the groups: zeros
+ */
+typedef struct ep_grouped_swiglu {
+    const void *x;
+    const uint8_t *x_scale;
+    int64_t x_rows;
+    const int32_t *rows;
+    int32_t rows_div;
+    int32_t groups;
+    const int32_t *offsets;
+    int64_t m, inter, k;
+    ep_matrix_t gate, up, slot_gate, slot_up;
+    const ep_layout_t *layout;
+    const float *weights;
+    int64_t weights_count;
+    uint8_t *h, *h_scale;
+    int32_t keep_dtype;
+    void *keep;
+    uint8_t *keep_scale;
+} ep_grouped_swiglu_t;
+int ep_grouped_swiglu(const ep_grouped_swiglu_t *p, ep_stream_t stream);
+
+/*
+ * Its gradient, from the gradient dy of the block's output (a row for each token)
+ * and from a, b as they were kept.  With d = down_g^T dy[r(i)], s = sigmoid(a):
+ *   da = w_i d b s (1 + a (1 - s)),  db = w_i d a s,  dw_i = sum over inter of d a s b
+ *   dy, dy_scale, dy_rows, rows, rows_div, groups, offsets, m, layout  as x and the
+ *            rest there; k columns (the block's output)
+ *   down, slot_down   [groups][inter][k]: the matrices back as ep_quant_blocks(transpose = 1)
+ *            writes them
+ *   keep, keep_dtype, keep_scale, weights  as ep_grouped_swiglu wrote or took them
+ *   grad     device bf16 [m][2 * inter]: da and then db, the dy of the weight gradient; or NULL
+ *   q, q_scale  the same in 8 bits in the layout of keep: the x of the grouped product
+ *            that gives the input gradient, with the matrices [groups][hidden][2 * I];
+ *            or NULL
+ *   grad_weights  device float or bf16 (grad_weights_dtype) [pairs], or NULL: dw at
+ *            i = pos[pair], 0 where pos is outside [0, m); pos NULL: dw_i, pairs == m.
+ *            d keeps about 16 bits (see ep_grouped_matmul's product), so does dw
+ *   ws       with grad_weights: ep_swiglu_backward_workspace_bytes(m, inter) bytes, 16-byte
+ *            aligned; no state between calls, calls in flight at once need their own
+ * Every element of the outputs is written; rows without a dy are zeros.
+ */
+typedef struct ep_grouped_swiglu_backward {
+    const void *dy;
+    const uint8_t *dy_scale;
+    int64_t dy_rows;
+    const int32_t *rows;
+    int32_t rows_div;
+    int32_t groups;
+    const int32_t *offsets;
+    int64_t m, inter, k;
+    ep_matrix_t down, slot_down;
+    const ep_layout_t *layout;
+    const float *weights;
+    int64_t weights_count;
+    int32_t keep_dtype;
+    const void *keep;
+    const uint8_t *keep_scale;
+    void *grad;
+    uint8_t *q, *q_scale;
+    void *grad_weights;
+    int32_t grad_weights_dtype;
+    const int32_t *pos;
+    int64_t pairs;
+    void *ws;
+    size_t ws_bytes;
+} ep_grouped_swiglu_backward_t;
+size_t ep_swiglu_backward_workspace_bytes(int64_t m, int64_t inter);
+int ep_grouped_swiglu_backward(const ep_grouped_swiglu_backward_t *p, ep_stream_t stream);
+
+/*
  * Combine: out_t = sum_j weights[t][j] * y[pos[t][j]] in fp32, j ascending,
  * rounded to bf16 once.  pos: device int32 [T][k] (dispatch_pos of
  * ep_dispatch_layout); positions outside [0, rows) give nothing.  y: bf16

@@ -1,0 +1,585 @@
+// The gated feed-forward block over groups of rows, forward and backward, on the
+// loop of the 8-bit grouped products (product.h).  For row i of group e, which
+// serves pair p of token t:
+//   forward   g = gate_e x_t,  u = up_e x_t,  h = w_p silu(g) u   in 8 bits
+//             and, for a backward pass, g and u kept in 8 bits or bf16
+//   backward  d = down_e^T dout_t,  s = sigmoid(g):
+//             dw_p = sum_n d g s u,  dg = w_p d u s (1 + g (1 - s)),  du = w_p d g s
+//             as bf16 (for the weight gradient) and in 8 bits (for the input gradient)
+// Both are one product whose tile becomes the outputs before it leaves the
+// registers: neither [g u] nor d is ever written in 16 bits and read again.
+#include "product.h"
+
+namespace ep {
+namespace {
+
+enum Keep { kNone, kSixteen, kEight };
+
+// ---- a lane's 16 values of a 32 x 32 fragment ----
+// Value e belongs to column 8 (e / 4) + 4 (lane / 32) + e % 4 of the fragment's
+// row lane % 32.  Memory wants 16 consecutive columns a lane, the lower lanes
+// the first ones: a swap between the halves of the wave goes either way.
+
+struct Two {
+    uint32_t a, b;
+};
+__device__ __forceinline__ Two swap_halves(uint32_t a, uint32_t b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    return Two{r[0], r[1]};
+}
+
+// four bytes for every 4 values, to and from 16 consecutive bytes
+__device__ __forceinline__ u32x4 bytes_to_memory(const u32x4 &v) {
+    const Two p = swap_halves(v[0], v[2]), q = swap_halves(v[1], v[3]);
+    return u32x4{p.a, p.b, q.a, q.b};
+}
+__device__ __forceinline__ u32x4 bytes_from_memory(const u32x4 &v) {
+    const Two p = swap_halves(v[0], v[1]), q = swap_halves(v[2], v[3]);
+    return u32x4{p.a, q.a, p.b, q.b};
+}
+
+struct Words {
+    u32x4 lo, hi;  // 8 columns each
+};
+// the same for 16-bit values, two a word
+__device__ __forceinline__ Words words_to_memory(const uint32_t (&v)[8]) {
+    const Two a = swap_halves(v[0], v[4]), b = swap_halves(v[1], v[5]), c = swap_halves(v[2], v[6]),
+              d = swap_halves(v[3], v[7]);
+    return Words{u32x4{a.a, b.a, a.b, b.b}, u32x4{c.a, d.a, c.b, d.b}};
+}
+__device__ __forceinline__ void words_from_memory(const Words &w, uint32_t (&v)[8]) {
+    const Two a = swap_halves(w.lo[0], w.lo[2]), b = swap_halves(w.lo[1], w.lo[3]), c = swap_halves(w.hi[0], w.hi[2]),
+              d = swap_halves(w.hi[1], w.hi[3]);
+    v[0] = a.a, v[4] = a.b, v[1] = b.a, v[5] = b.b, v[2] = c.a, v[6] = c.b, v[3] = d.a, v[7] = d.b;
+}
+
+__device__ __forceinline__ float other_half_max(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const Two t = swap_halves(b, b);
+    return fmaxf(__builtin_bit_cast(float, t.a), __builtin_bit_cast(float, t.b));
+}
+__device__ __forceinline__ float other_half_sum(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const Two t = swap_halves(b, b);
+    return __builtin_bit_cast(float, t.a) + __builtin_bit_cast(float, t.b);
+}
+
+// |v| for a block's scale: infinity * 0 is NaN, and fmaxf passes over NaN
+__device__ __forceinline__ float finite_max(float m, float v) { return fmaxf(m, fmaf(v, 0.0f, fabsf(v))); }
+
+// The upper halves of two floats, the lowest bit set where anything below is
+// ("round to odd"): rounding these 8 bits of mantissa to the 4 of 8-bit floating
+// point then gives what rounding the floats themselves does, bit for bit.
+__device__ __forceinline__ uint32_t odd_pair(float a, float b) {
+    uint32_t x = __builtin_bit_cast(uint32_t, a), y = __builtin_bit_cast(uint32_t, b);
+    x |= (x & 0xffffu) + 0xffffu;
+    y |= (y & 0xffffu) + 0xffffu;
+    return __builtin_amdgcn_perm(y, x, 0x07060302u);
+}
+
+__device__ __forceinline__ uint32_t four_bytes(float a, float b, float c, float d, float inv) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
+}
+// of a fragment held in odd pairs, in its memory order
+__device__ __forceinline__ u32x4 odd_to_memory(const uint32_t (&v)[8], float inv) {
+    u32x4 q;
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        q[e] = four_bytes(bf16_lo(v[2 * e]), bf16_hi(v[2 * e]), bf16_lo(v[2 * e + 1]), bf16_hi(v[2 * e + 1]), inv);
+    return bytes_to_memory(q);
+}
+
+// The sigmoid takes the hardware's exponential and reciprocal: 2^-16 of a value at
+// most, against the 2^-4 (8 bits) or 2^-9 (bf16) of the roundings that follow.
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+// 16 columns of a bf16 row from column n on, of which the row has N
+__device__ __forceinline__ void store_words(uint16_t *row, int n, int N, const Words &w) {
+    if (n + 16 <= N) {
+        *reinterpret_cast<u32x4_at2 *>(row + n) = w.lo;
+        *reinterpret_cast<u32x4_at2 *>(row + n + 8) = w.hi;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 16; q++) {
+            const u32x4 &v = q < 8 ? w.lo : w.hi;
+            if (n + q < N) row[n + q] = (uint16_t)(v[q % 8 / 2] >> (16 * (q % 2)));
+        }
+    }
+}
+__device__ __forceinline__ Words load_words(const uint16_t *row, int n, int N) {
+    Words w{{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if (n + 16 <= N) {
+        w.lo = *reinterpret_cast<const u32x4_at2 *>(row + n);
+        w.hi = *reinterpret_cast<const u32x4_at2 *>(row + n + 8);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 16; q++) {
+            u32x4 &v = q < 8 ? w.lo : w.hi;
+            if (n + q < N) v[q % 8 / 2] |= (uint32_t)row[n + q] << (16 * (q % 2));
+        }
+    }
+    return w;
+}
+
+// A row of scale bytes past its blocks, as ep_quant_rows writes it
+__device__ __forceinline__ void pad_scales(uint8_t *row, int blocks, int stride) {
+    for (int b = blocks; b < stride; b++) row[b] = 127;
+}
+
+// rows [m0, m1) of bytes in 8 bits and their scales, as rows of zeros have them
+__device__ __forceinline__ void zero_rows(uint8_t *q, uint8_t *scale, int blocks, int stride, int64_t m0, int64_t m1,
+                                          int64_t id, int64_t threads) {
+    for (int64_t i = m0 * blocks * 8 + id; i < m1 * blocks * 8; i += threads)
+        reinterpret_cast<u32x4 *>(q)[i] = u32x4{0, 0, 0, 0};
+    for (int64_t i = m0 * stride + id; i < m1 * stride; i += threads) scale[i] = i % stride < blocks ? 1 : 127;
+}
+__device__ __forceinline__ void zero_words(uint16_t *y, int64_t from, int64_t to, int64_t id, int64_t threads) {
+    for (int64_t i = from + id; i < to; i += threads) y[i] = 0;
+}
+
+// the weight of a tile's row, 1 without weights
+__device__ __forceinline__ float row_weight(const ProductArgs &A, const float *weights, int row, int place) {
+    return !weights ? 1.0f : place < 0 ? 0.0f : weights[A.rows ? A.rows[row] : row];
+}
+
+// ------------------------------------------------------------------ forward
+
+// A tile is 128 columns of gate and the same ones of up; a wave has the same half
+// (or quarter) of both, so that silu(g) u needs no exchange.  A block's scale does:
+// every wave puts the scale bytes of its part into LDS, and the largest counts.
+template <Keep kKeep>
+struct GatedTile {
+    static constexpr int kMatrices = 2;
+    struct Args {
+        SecondArgs up;
+        const float *weights;
+        uint8_t *h, *h_scale;
+        void *kept;
+        uint8_t *kept_scale;
+        int32_t ib, hs, ks;  // blocks of inter, bytes of a row of scales of h and of what is kept
+    };
+    template <int BM, int kWavesN>
+    struct Shared {
+        float weight[2][BM];
+        uint32_t codes[kWavesN][BM];
+    };
+
+    __device__ __forceinline__ static const SecondArgs &second(const Args &B) { return B.up; }
+
+    template <class S>
+    __device__ __forceinline__ static void locate(const ProductArgs &A, const Args &B, S &shared, int buf, int thread,
+                                                  int row, int place) {
+        shared.weight[buf][thread] = row_weight(A, B.weights, row, place);
+    }
+
+    template <int BM, int BN, int WM, int WN, int FM, int FN, class S>
+    __device__ __forceinline__ static void store(const ProductArgs &A, const Args &B, const ProductTile<2> &tile,
+                                                 const int32_t *places, S &shared, int buf, int wm, int wn, int l,
+                                                 f32x16 (&acc)[FN][FM]) {
+        constexpr int F = FN / 2, kWavesN = BN / WN;
+        const int b = tile.n0 / kScaleBlock, c0 = tile.n0 + wn * (WN / 2);
+        const bool whole = __builtin_amdgcn_readfirstlane(tile.n0 + kScaleBlock <= A.N);
+        uint32_t held[kKeep != kNone ? F : 1][FM][8];  // h in odd pairs, where g and u are still needed
+#pragma unroll
+        for (int j = 0; j < FM; j++) {
+            const int r = wm * WM + j * 32 + (l & 31);
+            const bool real = places[r] >= 0;
+            const float weight = shared.weight[buf][r];
+            float th = 0, tg = 0, tu = 0;
+#pragma unroll
+            for (int i = 0; i < F; i++) {
+                float h[16];
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    float g = acc[i][j][e], u = acc[F + i][j][e];
+                    if (!real || (!whole && c0 + i * 32 + e / 4 * 8 + (l >> 5) * 4 + e % 4 >= A.N)) g = u = 0.0f;
+                    h[e] = g * sigmoid(g) * u * weight;
+                    if (!real) h[e] = 0.0f;  // whatever its weight
+                    th = finite_max(th, h[e]);
+                    if constexpr (kKeep == kNone) {
+                        acc[i][j][e] = h[e];
+                    } else {
+                        acc[i][j][e] = g;
+                        acc[F + i][j][e] = u;
+                        tg = finite_max(tg, g);
+                        tu = finite_max(tu, u);
+                    }
+                }
+                if constexpr (kKeep != kNone)
+#pragma unroll
+                    for (int e = 0; e < 8; e++) held[i][j][e] = odd_pair(h[2 * e], h[2 * e + 1]);
+            }
+            uint32_t code = fp8_scale_code(other_half_max(th));
+            if constexpr (kKeep == kEight)
+                code |= fp8_scale_code(other_half_max(tg)) << 8 | fp8_scale_code(other_half_max(tu)) << 16;
+            if (l < 32) shared.codes[wn][r] = code;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < FM; j++) {
+            const int r = wm * WM + j * 32 + (l & 31), m = tile.m0 + r;
+            const bool in = m < tile.m1;
+            int ch = 0, cg = 0, cu = 0;
+#pragma unroll
+            for (int i = 0; i < kWavesN; i++) {
+                const uint32_t code = shared.codes[i][r];
+                ch = max(ch, (int)(code & 255));
+                cg = max(cg, (int)(code >> 8 & 255));
+                cu = max(cu, (int)(code >> 16));
+            }
+            const int64_t at = (int64_t)m * B.ib * kScaleBlock + c0 + (l >> 5) * 16;
+            const int64_t kept = at + (int64_t)m * B.ib * kScaleBlock;  // twice as far apart
+#pragma unroll
+            for (int i = 0; i < F; i++) {
+                u32x4 q;
+                if constexpr (kKeep == kNone) {
+                    q = bytes_of(acc[i][j], pow2_of(254 - ch));
+                } else {
+                    q = odd_to_memory(held[i][j], pow2_of(254 - ch));
+                }
+                if (in) *reinterpret_cast<u32x4 *>(B.h + at + i * 32) = q;
+                if constexpr (kKeep == kEight) {
+                    uint8_t *k = static_cast<uint8_t *>(B.kept) + kept + i * 32;
+                    const u32x4 g = bytes_of(acc[i][j], pow2_of(254 - cg));
+                    const u32x4 u = bytes_of(acc[F + i][j], pow2_of(254 - cu));
+                    if (in) {
+                        *reinterpret_cast<u32x4 *>(k) = g;
+                        *reinterpret_cast<u32x4 *>(k + B.ib * kScaleBlock) = u;
+                    }
+                }
+                if constexpr (kKeep == kSixteen) {
+                    uint16_t *k = static_cast<uint16_t *>(B.kept) + (int64_t)m * 2 * A.N;
+                    const int n = c0 + i * 32 + (l >> 5) * 16;
+                    const Words g = words_of(acc[i][j]), u = words_of(acc[F + i][j]);
+                    if (in) {
+                        store_words(k, n, A.N, g);
+                        store_words(k + A.N, n, A.N, u);
+                    }
+                }
+            }
+            if (in && wn == 0 && l < 32) {
+                uint8_t *hs = B.h_scale + (int64_t)m * B.hs;
+                hs[b] = (uint8_t)ch;
+                if (b == B.ib - 1) pad_scales(hs, B.ib, B.hs);
+                if constexpr (kKeep == kEight) {
+                    uint8_t *ks = B.kept_scale + (int64_t)m * B.ks;
+                    ks[b] = (uint8_t)cg;
+                    ks[B.ib + b] = (uint8_t)cu;
+                    if (b == B.ib - 1) pad_scales(ks, 2 * B.ib, B.ks);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ static u32x4 bytes_of(const f32x16 &v, float inv) {
+        u32x4 q;
+#pragma unroll
+        for (int e = 0; e < 4; e++) q[e] = four_bytes(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], inv);
+        return bytes_to_memory(q);
+    }
+    __device__ __forceinline__ static Words words_of(const f32x16 &v) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+        return words_to_memory(w);
+    }
+
+    // rows of zeros
+    __device__ __forceinline__ static void tail(const ProductArgs &A, const Args &B, int64_t id, int64_t threads) {
+        const int64_t m0 = A.groups.start(A.groups.G), m1 = A.groups.M;
+        zero_rows(B.h, B.h_scale, B.ib, B.hs, m0, m1, id, threads);
+        if constexpr (kKeep == kEight)
+            zero_rows(static_cast<uint8_t *>(B.kept), B.kept_scale, 2 * B.ib, B.ks, m0, m1, id, threads);
+        if constexpr (kKeep == kSixteen)
+            zero_words(static_cast<uint16_t *>(B.kept), m0 * 2 * A.N, m1 * 2 * A.N, id, threads);
+    }
+};
+
+// ----------------------------------------------------------------- backward
+
+// A wave's 128 columns are a block of dg and one of du, so its scales need no
+// exchange, and its share of dw is one number a row, added up by the second
+// kernel in the blocks' order.
+template <Keep kKeep>
+struct GatedBackTile {
+    static constexpr int kMatrices = 1;
+    struct Args {
+        const float *weights;
+        const void *kept;
+        const uint8_t *kept_scale;
+        uint16_t *dgu;           // or null
+        uint8_t *q, *q_scale;    // or null
+        float *dots;             // [rows][blocks], or null
+        int32_t ib, qs;          // blocks of inter, bytes of a row of scales
+    };
+    template <int BM, int kWavesN>
+    struct Shared {
+        float weight[2][BM];
+    };
+
+    template <class S>
+    __device__ __forceinline__ static void locate(const ProductArgs &A, const Args &B, S &shared, int buf, int thread,
+                                                  int row, int place) {
+        shared.weight[buf][thread] = row_weight(A, B.weights, row, place);
+    }
+
+    template <int BM, int BN, int WM, int WN, int FM, int FN, class S>
+    __device__ __forceinline__ static void store(const ProductArgs &A, const Args &B, const ProductTile<1> &tile,
+                                                 const int32_t *places, S &shared, int buf, int wm, int wn, int l,
+                                                 f32x16 (&acc)[FN][FM]) {
+        static_assert(WN == kScaleBlock, "a wave's columns are one block");
+        const int c0 = tile.n0 + wn * WN, b = c0 / kScaleBlock;
+        if (b >= B.ib) return;
+        const bool whole = __builtin_amdgcn_readfirstlane(c0 + WN <= A.N);
+        const int64_t wide = (int64_t)B.ib * kScaleBlock;
+#pragma unroll
+        for (int j = 0; j < FM; j++) {
+            const int r = wm * WM + j * 32 + (l & 31), m = tile.m0 + r;
+            const bool in = m < tile.m1, real = in && places[r] >= 0;
+            const int64_t row = in ? m : tile.m0;
+            const float weight = shared.weight[buf][r];
+            float gs = 1, us = 1;
+            if constexpr (kKeep == kEight) {
+                gs = pow2_of(B.kept_scale[row * B.qs + b]);
+                us = pow2_of(B.kept_scale[row * B.qs + B.ib + b]);
+            }
+            uint32_t vg[FN][8], vu[FN][8];
+            float tg = 0, tu = 0, dot = 0;
+#pragma unroll
+            for (int i = 0; i < FN; i++) {
+                const int n = c0 + i * 32 + (l >> 5) * 16;
+                float g[16], u[16];
+                if constexpr (kKeep == kEight) {
+                    const uint8_t *k = static_cast<const uint8_t *>(B.kept) + row * 2 * wide + n;
+                    const u32x4 a = bytes_from_memory(*reinterpret_cast<const u32x4 *>(k));
+                    const u32x4 c = bytes_from_memory(*reinterpret_cast<const u32x4 *>(k + wide));
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const auto g0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a[e], false);
+                        const auto g1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a[e], true);
+                        const auto u0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[e], false);
+                        const auto u1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[e], true);
+                        g[4 * e] = g0[0] * gs, g[4 * e + 1] = g0[1] * gs, g[4 * e + 2] = g1[0] * gs, g[4 * e + 3] = g1[1] * gs;
+                        u[4 * e] = u0[0] * us, u[4 * e + 1] = u0[1] * us, u[4 * e + 2] = u1[0] * us, u[4 * e + 3] = u1[1] * us;
+                    }
+                } else {
+                    const uint16_t *k = static_cast<const uint16_t *>(B.kept) + row * 2 * A.N;
+                    uint32_t a[8], c[8];
+                    words_from_memory(load_words(k, n, A.N), a);
+                    words_from_memory(load_words(k + A.N, n, A.N), c);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        g[2 * e] = bf16_lo(a[e]), g[2 * e + 1] = bf16_hi(a[e]);
+                        u[2 * e] = bf16_lo(c[e]), u[2 * e + 1] = bf16_hi(c[e]);
+                    }
+                }
+                float dg[16], du[16];
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    const float d = acc[i][j][e], s = sigmoid(g[e]), act = g[e] * s, dw = d * weight;
+                    float x = dw * u[e] * (s * (1.0f + g[e] * (1.0f - s))), y = dw * act, z = d * (act * u[e]);
+                    if (!real || (!whole && c0 + i * 32 + e / 4 * 8 + (l >> 5) * 4 + e % 4 >= A.N)) x = y = z = 0.0f;
+                    dg[e] = x;
+                    du[e] = y;
+                    dot += z;
+                    tg = finite_max(tg, x);
+                    tu = finite_max(tu, y);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    vg[i][e] = odd_pair(dg[2 * e], dg[2 * e + 1]);
+                    vu[i][e] = odd_pair(du[2 * e], du[2 * e + 1]);
+                }
+                if (B.dgu) {
+                    uint32_t wg[8], wu[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        wg[e] = pack_bf16(dg[2 * e], dg[2 * e + 1]);
+                        wu[e] = pack_bf16(du[2 * e], du[2 * e + 1]);
+                    }
+                    const Words a = words_to_memory(wg), c = words_to_memory(wu);
+                    uint16_t *o = B.dgu + row * 2 * A.N;
+                    if (in) {
+                        store_words(o, n, A.N, a);
+                        store_words(o + A.N, n, A.N, c);
+                    }
+                }
+            }
+            if (B.q) {
+                const int cg = fp8_scale_code(other_half_max(tg)), cu = fp8_scale_code(other_half_max(tu));
+                uint8_t *q = B.q + row * 2 * wide + c0 + (l >> 5) * 16;
+#pragma unroll
+                for (int i = 0; i < FN; i++) {
+                    const u32x4 a = odd_to_memory(vg[i], pow2_of(254 - cg)), c = odd_to_memory(vu[i], pow2_of(254 - cu));
+                    if (in) {
+                        *reinterpret_cast<u32x4 *>(q + i * 32) = a;
+                        *reinterpret_cast<u32x4 *>(q + wide + i * 32) = c;
+                    }
+                }
+                if (in && l < 32) {
+                    uint8_t *s = B.q_scale + row * B.qs;
+                    s[b] = (uint8_t)cg;
+                    s[B.ib + b] = (uint8_t)cu;
+                    if (b == B.ib - 1) pad_scales(s, 2 * B.ib, B.qs);
+                }
+            }
+            if (B.dots) {
+                const float sum = other_half_sum(dot);
+                if (in && l < 32) B.dots[row * B.ib + b] = sum;
+            }
+        }
+    }
+
+    // rows of zeros
+    __device__ __forceinline__ static void tail(const ProductArgs &A, const Args &B, int64_t id, int64_t threads) {
+        const int64_t m0 = A.groups.start(A.groups.G), m1 = A.groups.M;
+        if (B.dgu) zero_words(B.dgu, m0 * 2 * A.N, m1 * 2 * A.N, id, threads);
+        if (B.q) zero_rows(B.q, B.q_scale, 2 * B.ib, B.qs, m0, m1, id, threads);
+        if (B.dots)
+            for (int64_t i = m0 * B.ib + id; i < m1 * B.ib; i += threads) B.dots[i] = 0.0f;
+    }
+};
+
+// dw of each pair: its position's blocks in order, in fp32; 0 without a position
+constexpr int kDotThreads = 256;
+template <bool kBf16>
+__global__ __launch_bounds__(kDotThreads) void pair_dots_kernel(const float *__restrict__ dots, int ib, int64_t m,
+                                                                const int32_t *__restrict__ pos, int64_t pairs,
+                                                                void *__restrict__ out) {
+    const int64_t i = (int64_t)blockIdx.x * kDotThreads + threadIdx.x;
+    if (i >= pairs) return;
+    const int64_t p = pos ? pos[i] : i;
+    float s = 0.0f;
+    if (p >= 0 && p < m)
+        for (int b = 0; b < ib; b++) s += dots[p * ib + b];
+    if constexpr (kBf16) static_cast<uint16_t *>(out)[i] = to_bf16(s);
+    else static_cast<float *>(out)[i] = s;
+}
+
+template <Keep kKeep>
+hipError_t forward(const ProductArgs &A, const typename GatedTile<kNone>::Args &B, hipStream_t s) {
+    typedef GatedTile<kKeep> Tile;
+    const typename Tile::Args C{B.up, B.weights, B.h, B.h_scale, B.kept, B.kept_scale, B.ib, B.hs, B.ks};
+    const int64_t rows = A.groups.M / A.groups.G;
+    auto enough = [&](int64_t tile) { return ceil_div(A.groups.M, tile) * ceil_div(A.N, kScaleBlock) >= 192; };
+    if (rows >= 256 && enough(256)) return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
+    if (rows >= 96) return launch_product<Tile, 128, 256, 64, 128, 4>(A, C, s);
+    return launch_product<Tile, 64, 256, 64, 64, 6>(A, C, s);
+}
+
+template <Keep kKeep>
+hipError_t backward(const ProductArgs &A, const typename GatedBackTile<kEight>::Args &B, hipStream_t s) {
+    typedef GatedBackTile<kKeep> Tile;
+    const typename Tile::Args C{B.weights, B.kept, B.kept_scale, B.dgu, B.q, B.q_scale, B.dots, B.ib, B.qs};
+    const int64_t rows = A.groups.M / A.groups.G;
+    auto enough = [&](int64_t tile) { return ceil_div(A.groups.M, tile) * ceil_div(A.N, tile) >= 192; };
+    if (rows >= 256 && enough(256)) return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
+    if (rows >= 96) return launch_product<Tile, 128, 128, 32, 128, 4>(A, C, s);
+    return launch_product<Tile, 64, 128, 32, 128, 6>(A, C, s);
+}
+
+// what a matrix argument becomes
+struct Matrix {
+    const uint8_t *w, *ws, *slot_w, *slot_ws;
+    int64_t w_stride, ws_stride, slot_w_stride, slot_ws_stride;
+    Matrix(const ep_matrix_t &m, const ep_matrix_t &slot)
+        : w(static_cast<const uint8_t *>(m.data)), ws(m.scale), slot_w(static_cast<const uint8_t *>(slot.data)),
+          slot_ws(slot.scale), w_stride(m.stride), ws_stride(m.scale_stride), slot_w_stride(slot.stride),
+          slot_ws_stride(slot.scale_stride) {}
+};
+
+void set_matrix(ProductArgs *A, const Matrix &m) {
+    A->w = m.w, A->ws = m.ws, A->slot_w = m.slot_w, A->slot_ws = m.slot_ws;
+    A->w_stride = m.w_stride, A->ws_stride = m.ws_stride;
+    A->slot_w_stride = m.slot_w_stride, A->slot_ws_stride = m.slot_ws_stride;
+}
+
+bool keep_dtype(int32_t d) { return d == EP_DTYPE_BF16 || d == EP_DTYPE_FP8; }
+
+// what is kept, or was: bf16 [m][2 inter], or bytes with their scales
+bool kept_ok(int32_t dtype, const void *kept, const uint8_t *scale) {
+    return dtype == EP_DTYPE_BF16 ? kept && is_aligned(kept, 2)
+                                  : kept && scale && is_aligned(kept, 16) && is_aligned(scale, 4);
+}
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_grouped_swiglu(const ep_grouped_swiglu_t *p, ep_stream_t stream) {
+    if (!p) return EP_ERR_INVALID_ARG;
+    const ProductShape shape{p->x, p->x_scale, p->x_rows, p->rows, p->rows_div, p->groups, p->offsets, p->m, p->inter,
+                             p->k, p->weights, p->weights_count};
+    if (!product_sizes_ok(shape) || (p->keep && !keep_dtype(p->keep_dtype))) return EP_ERR_INVALID_ARG;
+    if (p->m == 0) return EP_OK;
+    const bool slots = p->slot_gate.data && p->slot_gate.scale && p->slot_up.data && p->slot_up.scale;
+    ProductArgs A;
+    if (!product_args(shape, p->layout, slots, &A) ||
+        !product_matrix_ok(p->gate, p->slot_gate, p->layout, p->groups, p->inter, p->k) ||
+        !product_matrix_ok(p->up, p->slot_up, p->layout, p->groups, p->inter, p->k))
+        return EP_ERR_INVALID_ARG;
+    if (!p->h || !p->h_scale || !is_aligned(p->h, 16) || !is_aligned(p->h_scale, 4) ||
+        (p->keep && !kept_ok(p->keep_dtype, p->keep, p->keep_scale)))
+        return EP_ERR_INVALID_ARG;
+    set_matrix(&A, Matrix(p->gate, p->slot_gate));
+    const Matrix up(p->up, p->slot_up);
+    const int ib = (int)ceil_div(p->inter, kScaleBlock);
+    const GatedTile<kNone>::Args B{
+        SecondArgs{up.w, up.ws, up.slot_w, up.slot_ws, up.w_stride, up.ws_stride, up.slot_w_stride, up.slot_ws_stride},
+        p->weights, p->h, p->h_scale, p->keep, p->keep_scale, ib, (int32_t)ep_scale_stride(p->inter),
+        (int32_t)ep_scale_stride((int64_t)2 * ib * kScaleBlock)};
+    const hipStream_t s = to_stream(stream);
+    if (!p->keep) return rc_of(forward<kNone>(A, B, s));
+    return rc_of(p->keep_dtype == EP_DTYPE_BF16 ? forward<kSixteen>(A, B, s) : forward<kEight>(A, B, s));
+}
+
+extern "C" size_t ep_swiglu_backward_workspace_bytes(int64_t m, int64_t inter) {
+    if (m < 1 || m > kMaxRows || inter < 1 || inter > (1 << 24)) return 0;
+    return (size_t)m * (size_t)ceil_div(inter, kScaleBlock) * sizeof(float);
+}
+
+extern "C" int ep_grouped_swiglu_backward(const ep_grouped_swiglu_backward_t *p, ep_stream_t stream) {
+    if (!p) return EP_ERR_INVALID_ARG;
+    const ProductShape shape{p->dy, p->dy_scale, p->dy_rows, p->rows, p->rows_div, p->groups, p->offsets, p->m,
+                             p->inter, p->k, p->weights, p->weights_count};
+    if (!product_sizes_ok(shape) || !keep_dtype(p->keep_dtype)) return EP_ERR_INVALID_ARG;
+    if (p->grad_weights && (!float_dtype(p->grad_weights_dtype) || p->pairs < 0 || p->pairs > (int64_t)1 << 38 ||
+                            !is_aligned(p->grad_weights, p->grad_weights_dtype == EP_DTYPE_BF16 ? 2 : 4) ||
+                            !is_aligned(p->pos, 4) || (!p->pos && p->pairs != p->m)))
+        return EP_ERR_INVALID_ARG;
+    if (p->m > 0) {
+        ProductArgs A;
+        if (!product_args(shape, p->layout, p->slot_down.data && p->slot_down.scale, &A) ||
+            !product_matrix_ok(p->down, p->slot_down, p->layout, p->groups, p->inter, p->k))
+            return EP_ERR_INVALID_ARG;
+        if (!kept_ok(p->keep_dtype, p->keep, p->keep_scale) || !is_aligned(p->grad, 2) ||
+            (!p->q != !p->q_scale) || !is_aligned(p->q, 16) || !is_aligned(p->q_scale, 4) ||
+            (!p->grad && !p->q && !p->grad_weights))
+            return EP_ERR_INVALID_ARG;
+        if (p->grad_weights && (!p->ws || !is_aligned(p->ws, 16) ||
+                                p->ws_bytes < ep_swiglu_backward_workspace_bytes(p->m, p->inter)))
+            return EP_ERR_INVALID_ARG;
+        set_matrix(&A, Matrix(p->down, p->slot_down));
+        const int ib = (int)ceil_div(p->inter, kScaleBlock);
+        const GatedBackTile<kEight>::Args B{p->weights, p->keep, p->keep_scale, static_cast<uint16_t *>(p->grad), p->q,
+                                            p->q_scale, p->grad_weights ? static_cast<float *>(p->ws) : nullptr, ib,
+                                            (int32_t)ep_scale_stride((int64_t)2 * ib * kScaleBlock)};
+        const hipStream_t s = to_stream(stream);
+        const hipError_t e = p->keep_dtype == EP_DTYPE_BF16 ? backward<kSixteen>(A, B, s) : backward<kEight>(A, B, s);
+        if (e != hipSuccess) return EP_ERR_HIP;
+    }
+    if (p->grad_weights && p->pairs > 0) {
+        const int64_t blocks = ceil_div(p->pairs, kDotThreads);
+        if (blocks > kMaxBlocks) return EP_ERR_INVALID_ARG;
+        const int ib = (int)ceil_div(p->inter, kScaleBlock);
+        auto run = [&](auto kernel) {
+            kernel<<<(uint32_t)blocks, kDotThreads, 0, to_stream(stream)>>>(static_cast<const float *>(p->ws), ib, p->m,
+                                                                            p->pos, p->pairs, p->grad_weights);
+        };
+        p->grad_weights_dtype == EP_DTYPE_BF16 ? run(pair_dots_kernel<true>) : run(pair_dots_kernel<false>);
+        return rc_of(hipGetLastError());
+    }
+    return EP_OK;
+}

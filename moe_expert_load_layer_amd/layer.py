@@ -44,6 +44,28 @@ class _CWgrad(ctypes.Structure):
                 ("slot_out", _vp), ("out_stride", _i64), ("slot_out_stride", _i64)]
 
 
+class _CSwiglu(ctypes.Structure):
+    _fields_ = [("x", _vp), ("x_scale", _vp), ("x_rows", _i64), ("rows", _vp), ("rows_div", _i32), ("groups", _i32),
+                ("offsets", _vp), ("m", _i64), ("inter", _i64), ("k", _i64), ("gate", _CMatrix), ("up", _CMatrix),
+                ("slot_gate", _CMatrix), ("slot_up", _CMatrix), ("layout", ctypes.POINTER(_CLayout)), ("weights", _vp),
+                ("weights_count", _i64), ("h", _vp), ("h_scale", _vp), ("keep_dtype", _i32), ("keep", _vp), ("keep_scale", _vp)]
+
+
+class _CSwigluBackward(ctypes.Structure):
+    _fields_ = [("dy", _vp), ("dy_scale", _vp), ("dy_rows", _i64), ("rows", _vp), ("rows_div", _i32), ("groups", _i32),
+                ("offsets", _vp), ("m", _i64), ("inter", _i64), ("k", _i64), ("down", _CMatrix), ("slot_down", _CMatrix),
+                ("layout", ctypes.POINTER(_CLayout)), ("weights", _vp), ("weights_count", _i64), ("keep_dtype", _i32),
+                ("keep", _vp), ("keep_scale", _vp), ("grad", _vp), ("q", _vp), ("q_scale", _vp), ("grad_weights", _vp),
+                ("grad_weights_dtype", _i32), ("pos", _vp), ("pairs", _i64), ("ws", _vp), ("ws_bytes", _sz)]
+
+
+class _CWgradMixed(ctypes.Structure):
+    _fields_ = [("dy", _vp), ("dy_rows", _i64), ("dy_stride", _i64), ("x", _vp), ("x_scale", _vp), ("x_rows", _i64),
+                ("dy_places", _vp), ("x_places", _vp), ("rows_div", _i32), ("groups", _i32), ("offsets", _vp),
+                ("m", _i64), ("n", _i64), ("k", _i64), ("layout", ctypes.POINTER(_CLayout)), ("out", _vp),
+                ("slot_out", _vp), ("out_stride", _i64), ("slot_out_stride", _i64)]
+
+
 class _CExperts(ctypes.Structure):
     _fields_ = [("hidden", _i32), ("inter", _i32), ("dtype", _i32), ("gate", _CMatrix), ("up", _CMatrix),
                 ("down", _CMatrix)]
@@ -67,6 +89,11 @@ def declare(L: ctypes.CDLL) -> None:
     L.ep_quant_blocks.argtypes = [_vp, _i32, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]
     L.ep_grouped_matmul.argtypes = [p(_CMatmul), _vp]
     L.ep_grouped_wgrad.argtypes = [p(_CWgrad), _vp]
+    L.ep_grouped_wgrad_mixed.argtypes = [p(_CWgradMixed), _vp]
+    L.ep_grouped_swiglu.argtypes = [p(_CSwiglu), _vp]
+    L.ep_swiglu_backward_workspace_bytes.argtypes = [_i64, _i64]
+    L.ep_swiglu_backward_workspace_bytes.restype = _sz
+    L.ep_grouped_swiglu_backward.argtypes = [p(_CSwigluBackward), _vp]
     L.ep_moe_combine.argtypes = [_vp, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _vp]
     L.ep_few_tokens_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32]
     L.ep_few_tokens_workspace_bytes.restype = _sz
@@ -75,8 +102,8 @@ def declare(L: ctypes.CDLL) -> None:
     L.ep_adamw_step.argtypes = [_vp, _i32, p(_CAdamW), _vp]
     L.ep_adamw_values.argtypes = [_vp, _i32, _vp, _vp, _vp]
     for f in ("ep_gate_topk", "ep_gate_topk_backward", "ep_quant_rows", "ep_swiglu_quant", "ep_quant_blocks",
-              "ep_grouped_matmul", "ep_grouped_wgrad", "ep_moe_combine", "ep_moe_few_tokens", "ep_adamw_step",
-              "ep_adamw_values"):
+              "ep_grouped_matmul", "ep_grouped_wgrad", "ep_grouped_wgrad_mixed", "ep_grouped_swiglu",
+              "ep_grouped_swiglu_backward", "ep_moe_combine", "ep_moe_few_tokens", "ep_adamw_step", "ep_adamw_values"):
         getattr(L, f).restype = ctypes.c_int
 
 
@@ -296,6 +323,17 @@ def ep_grouped_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w
     return y
 
 
+def _gradient(t: Optional[torch.Tensor], shape, device, name: str, stream) -> torch.Tensor:
+    """float32 [matrices][N][K], the matrices contiguous but perhaps apart."""
+    if t is None:
+        return _held(torch.empty(shape, dtype=torch.float32, device=device), stream)
+    if not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != shape:
+        raise EPBalanceError(f"{name} must be a float32 device tensor of shape {shape}")
+    if shape[0] and not t[0].is_contiguous():
+        raise EPBalanceError(f"{name} must have contiguous matrices")
+    return t
+
+
 def ep_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: Optional[torch.Tensor] = None,
                      layout: Optional[Layout] = None, out=None, slot_out=None, stream=None):
     """sum over the rows i of group g of dy[i][n] x[i][k] -> float32 [G][N][K]; dy, x bf16.
@@ -311,25 +349,202 @@ def ep_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: Optional[torch.
     G = _groups(offsets, layout, layout.num_experts if layout is not None else
                 1 if offsets is None else offsets.shape[0] - 1)
 
-    def gradient(t, count, name):
-        if t is None:
-            return _held(torch.empty((count, N, K), dtype=torch.float32, device=dy.device), stream)
-        if not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != (count, N, K):
-            raise EPBalanceError(f"{name} must be a float32 device tensor of shape {(count, N, K)}")
-        if count and not t[0].is_contiguous():
-            raise EPBalanceError(f"{name} must have contiguous matrices")
-        return t
-
-    out = gradient(out, layout.num_experts if layout is not None else G, "out")
+    shape = (layout.num_experts if layout is not None else G, N, K)
+    out = _gradient(out, shape, dy.device, "out", stream)
     p = _CWgrad(dy.data_ptr(), x.data_ptr(), ds, xs, M, N, K, G, None if offsets is None else offsets.data_ptr(),
                 None, out.data_ptr(), None, out.stride(0), 0)
     if layout is not None:
         p.layout = ctypes.pointer(layout.c)
-        slot_out = gradient(slot_out, layout.num_spare, "slot_out")
+        slot_out = _gradient(slot_out, (layout.num_spare, N, K), dy.device, "slot_out", stream)
         if layout.num_spare:
             p.slot_out, p.slot_out_stride = slot_out.data_ptr(), slot_out.stride(0)
     _check(lib().ep_grouped_wgrad(ctypes.byref(p), _stream(stream)), "ep_grouped_wgrad")
     return out if layout is None else (out, slot_out)
+
+
+def _places(t: Optional[torch.Tensor], name: str) -> int:
+    """The length of a list of places, int32 [rows]."""
+    if t.dim() != 1:
+        raise EPBalanceError(f"{name} must be [output rows]")
+    _arg(t, torch.int32, t.shape, name)
+    return t.shape[0]
+
+
+def ep_grouped_wgrad_mixed(dy: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
+                           offsets: Optional[torch.Tensor] = None, cols: Optional[int] = None, dy_rows=None,
+                           x_rows=None, rows_div: int = 1, layout: Optional[Layout] = None, out=None, slot_out=None,
+                           stream=None):
+    """ep_grouped_wgrad with x in 8 bits: sum over the rows i of group g of dy[d(i)][n] x[r(i)][k] -> float32 [G][N][cols].
+
+    x, x_scale as ep_quant_rows or ep_grouped_swiglu wrote rows of `cols` values (default: all that x has).
+    d(i) = dy_rows[i] // rows_div, r(i) = x_rows[i] // rows_div (int32 [M]; None: i; both: the same list; negative or
+    too large: the row adds nothing).  With a layout: (native, spare), as ep_grouped_wgrad."""
+    ds = _rows(dy, (torch.bfloat16,), "dy")
+    if x.dim() != 2 or x.shape[1] % 128:
+        raise EPBalanceError(f"x must be [rows][columns up to a multiple of 128], got shape {tuple(x.shape)}")
+    K, N = x.shape[1] if cols is None else cols, dy.shape[1]
+    if K < 1 or _up128(K) != x.shape[1]:
+        raise EPBalanceError(f"cols must be the columns that x's {x.shape[1]} hold, got {cols}")
+    _arg(x, _FP8, x.shape, "x")
+    _arg(x_scale, torch.uint8, (x.shape[0], ep_scale_stride(K)), "x_scale")
+    lengths = {name: t.shape[0] if places is None else _places(places, name + "_rows")
+               for name, t, places in (("dy", dy, dy_rows), ("x", x, x_rows))}
+    M = lengths["dy"]
+    if lengths["x"] != M:
+        raise EPBalanceError(f"dy and x must give the same rows, got {M} and {lengths['x']}")
+    if dy_rows is not None and x_rows is not None and dy_rows.data_ptr() != x_rows.data_ptr():
+        raise EPBalanceError("dy_rows and x_rows must be one list where both are given")
+    if offsets is not None and (offsets.dim() != 1 or offsets.shape[0] < 2):
+        raise EPBalanceError("offsets must be [groups + 1]")
+    G = _groups(offsets, layout, layout.num_experts if layout is not None else
+                1 if offsets is None else offsets.shape[0] - 1)
+    shape = (layout.num_experts if layout is not None else G, N, K)
+    out = _gradient(out, shape, dy.device, "out", stream)
+    p = _CWgradMixed(dy.data_ptr(), dy.shape[0], ds, x.data_ptr(), x_scale.data_ptr(), x.shape[0],
+                     None if dy_rows is None else dy_rows.data_ptr(), None if x_rows is None else x_rows.data_ptr(),
+                     rows_div, G, None if offsets is None else offsets.data_ptr(), M, N, K, None, out.data_ptr(), None,
+                     out.stride(0), 0)
+    if layout is not None:
+        p.layout = ctypes.pointer(layout.c)
+        slot_out = _gradient(slot_out, (layout.num_spare, N, K), dy.device, "slot_out", stream)
+        if layout.num_spare:
+            p.slot_out, p.slot_out_stride = slot_out.data_ptr(), slot_out.stride(0)
+    _check(lib().ep_grouped_wgrad_mixed(ctypes.byref(p), _stream(stream)), "ep_grouped_wgrad_mixed")
+    return out if layout is None else (out, slot_out)
+
+
+def _slot_matrix(layout: Layout, data, scale, rows: int, cols: int, name: str) -> _CMatrix:
+    if data is None or scale is None or data.shape[0] != layout.num_spare:
+        raise EPBalanceError(f"{name} and its scale must hold the layout's {layout.num_spare} spare slots")
+    return _matrix(data, scale, rows, cols, name)
+
+
+def _pair_weights(weights: torch.Tensor, count: Optional[int]) -> int:
+    """The length of float32 weights, one for each pair; count: what it has to be."""
+    if weights.dim() != 1:
+        raise EPBalanceError(f"weights must be [pairs], got shape {tuple(weights.shape)}")
+    _arg(weights, torch.float32, weights.shape if count is None else (count,), "weights")
+    return weights.shape[0]
+
+
+def ep_grouped_swiglu(x: torch.Tensor, x_scale: torch.Tensor, gate: torch.Tensor, gate_scale: torch.Tensor,
+                      up: torch.Tensor, up_scale: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                      rows: Optional[torch.Tensor] = None, rows_div: int = 1, weights: Optional[torch.Tensor] = None,
+                      keep: Optional[torch.dtype] = None, layout: Optional[Layout] = None, slot_gate=None,
+                      slot_gate_scale=None, slot_up=None, slot_up_scale=None, h=None, h_scale=None, kept=None,
+                      kept_scale=None, stream=None):
+    """h[i] = w_i silu(gate_g x[r(i)]) * (up_g x[r(i)]) in 8 bits, for the rows i of group g, in one product.
+
+    x, x_scale from ep_quant_rows, gate and up [G][I][K up to 128] with the scales of ep_quant_blocks; offsets, rows,
+    rows_div and layout as for ep_grouped_matmul.  weights float32, one for each pair that rows may name (a pair past
+    them has no input; without rows: [M]); None: 1.  keep: None, or the type in which the two products are kept for
+    ep_grouped_swiglu_backward, torch.bfloat16 ([M][2 I]) or torch.float8_e4m3fn ([M][2 * (I up to 128)] and scales).
+    Returns (h, h_scale, kept, kept_scale), the last two None where there are none."""
+    if x.dim() != 2 or gate.dim() != 3 or x.shape[1] % 128 or x.shape[1] != gate.shape[2]:
+        raise EPBalanceError(f"x [rows][k] and gate [groups][inter][k] must share k, a multiple of 128: got "
+                             f"{tuple(x.shape)} and {tuple(gate.shape)}")
+    X, K, I = x.shape[0], x.shape[1], gate.shape[1]
+    _arg(x, _FP8, x.shape, "x")
+    _arg(x_scale, torch.uint8, (X, ep_scale_stride(K)), "x_scale")
+    if up.shape != gate.shape:
+        raise EPBalanceError(f"gate and up must have one shape, got {tuple(gate.shape)} and {tuple(up.shape)}")
+    if gate_scale is None or up_scale is None:
+        raise EPBalanceError("gate_scale and up_scale are required")
+    G = _groups(offsets, layout, gate.shape[0])
+    M = X if rows is None else _places(rows, "rows")
+    count = 0 if weights is None else _pair_weights(weights, None if rows is not None else M)
+    h = _out(h, _FP8, (M, _up128(I)), x.device, "h", stream)
+    h_scale = _out(h_scale, torch.uint8, (M, ep_scale_stride(I)), x.device, "h_scale", stream)
+    if keep is None:
+        if kept is not None or kept_scale is not None:
+            raise EPBalanceError("kept needs keep, its type")
+    elif keep is torch.bfloat16:
+        kept = _out(kept, keep, (M, 2 * I), x.device, "kept", stream)
+        kept_scale = None
+    elif keep is _FP8:
+        kept = _out(kept, keep, (M, 2 * _up128(I)), x.device, "kept", stream)
+        kept_scale = _out(kept_scale, torch.uint8, (M, ep_scale_stride(2 * _up128(I))), x.device, "kept_scale", stream)
+    else:
+        raise EPBalanceError(f"keep must be None, torch.bfloat16 or torch.float8_e4m3fn, got {keep}")
+    p = _CSwiglu(x.data_ptr(), x_scale.data_ptr(), X, None if rows is None else rows.data_ptr(), rows_div, G,
+                 None if offsets is None else offsets.data_ptr(), M, I, K, _matrix(gate, gate_scale, I, K, "gate"),
+                 _matrix(up, up_scale, I, K, "up"), _CMatrix(), _CMatrix(), None,
+                 None if weights is None else weights.data_ptr(), count, h.data_ptr(), h_scale.data_ptr(),
+                 EP_DTYPE_FP8 if keep is _FP8 else EP_DTYPE_BF16, None if kept is None else kept.data_ptr(),
+                 None if kept_scale is None else kept_scale.data_ptr())
+    if layout is not None:
+        p.layout = ctypes.pointer(layout.c)
+        if layout.num_spare:
+            p.slot_gate = _slot_matrix(layout, slot_gate, slot_gate_scale, I, K, "slot_gate")
+            p.slot_up = _slot_matrix(layout, slot_up, slot_up_scale, I, K, "slot_up")
+    _check(lib().ep_grouped_swiglu(ctypes.byref(p), _stream(stream)), "ep_grouped_swiglu")
+    return h, h_scale, kept, kept_scale
+
+
+def ep_swiglu_backward_workspace_bytes(rows: int, inter: int) -> int:
+    return int(lib().ep_swiglu_backward_workspace_bytes(int(rows), int(inter)))
+
+
+def ep_grouped_swiglu_backward(dy: torch.Tensor, dy_scale: torch.Tensor, down: torch.Tensor, down_scale: torch.Tensor,
+                               kept: torch.Tensor, kept_scale: Optional[torch.Tensor] = None,
+                               offsets: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+                               rows_div: int = 1, weights: Optional[torch.Tensor] = None,
+                               pos: Optional[torch.Tensor] = None, weights_dtype: torch.dtype = torch.float32,
+                               layout: Optional[Layout] = None, slot_down=None, slot_down_scale=None, grad=None, q=None,
+                               q_scale=None, grad_weights=None, ws=None, stream=None):
+    """The gradient of ep_grouped_swiglu, from the gradient of the block's output and what was kept.
+
+    dy, dy_scale: the output's gradient, a row for each token, from ep_quant_rows; down [G][I][columns of dy] and its
+    scales from ep_quant_blocks(transpose=True); kept, kept_scale, weights, offsets, rows, rows_div, layout as there.
+    Returns (grad bf16 [M][2 I], the dy of the projections' weight gradient; q and q_scale, the same in 8 bits
+    [M][2 * (I up to 128)], the x of the grouped product that gives the input gradient; grad_weights).  grad_weights,
+    where weights are given: in weights_dtype, float32 or bfloat16, by pair where pos (int32, each pair's position)
+    is given, else by position; from the 8-bit product, whose sums keep about 16 bits."""
+    if dy.dim() != 2 or down.dim() != 3 or dy.shape[1] % 128 or dy.shape[1] != down.shape[2]:
+        raise EPBalanceError(f"dy [rows][k] and down [groups][inter][k] must share k, a multiple of 128: got "
+                             f"{tuple(dy.shape)} and {tuple(down.shape)}")
+    X, K, I = dy.shape[0], dy.shape[1], down.shape[1]
+    _arg(dy, _FP8, dy.shape, "dy")
+    _arg(dy_scale, torch.uint8, (X, ep_scale_stride(K)), "dy_scale")
+    if down_scale is None:
+        raise EPBalanceError("down_scale is required")
+    if weights_dtype not in _FLOATS:
+        raise EPBalanceError(f"weights_dtype must be float32 or bfloat16, got {weights_dtype}")
+    G = _groups(offsets, layout, down.shape[0])
+    M = X if rows is None else _places(rows, "rows")
+    wide = 2 * _up128(I)
+    fp8 = kept_scale is not None
+    _arg(kept, _FP8 if fp8 else torch.bfloat16, (M, wide if fp8 else 2 * I), "kept")
+    if fp8:
+        _arg(kept_scale, torch.uint8, (M, ep_scale_stride(wide)), "kept_scale")
+    grad = _out(grad, torch.bfloat16, (M, 2 * I), dy.device, "grad", stream)
+    q = _out(q, _FP8, (M, wide), dy.device, "q", stream)
+    q_scale = _out(q_scale, torch.uint8, (M, ep_scale_stride(wide)), dy.device, "q_scale", stream)
+    p = _CSwigluBackward(dy.data_ptr(), dy_scale.data_ptr(), X, None if rows is None else rows.data_ptr(), rows_div, G,
+                         None if offsets is None else offsets.data_ptr(), M, I, K,
+                         _matrix(down, down_scale, I, K, "down"), _CMatrix(), None, None, 0,
+                         EP_DTYPE_FP8 if fp8 else EP_DTYPE_BF16, kept.data_ptr(),
+                         kept_scale.data_ptr() if fp8 else None, grad.data_ptr(), q.data_ptr(), q_scale.data_ptr())
+    if weights is not None:
+        p.weights_count = _pair_weights(weights, None if rows is not None else M)
+        pairs = M if pos is None else _places(pos, "pos")
+        grad_weights = _out(grad_weights, weights_dtype, (pairs,), dy.device, "grad_weights", stream)
+        need = ep_swiglu_backward_workspace_bytes(M, I)
+        if ws is None:
+            ws = _held(torch.empty(max(16, need), dtype=torch.uint8, device=dy.device), stream)
+        elif not (ws.is_cuda and ws.is_contiguous()):
+            raise EPBalanceError("ws must be a contiguous device tensor")
+        p.weights, p.grad_weights, p.grad_weights_dtype = weights.data_ptr(), grad_weights.data_ptr(), _FLOATS[weights_dtype]
+        p.pos, p.pairs = None if pos is None else pos.data_ptr(), pairs
+        p.ws, p.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    elif pos is not None or grad_weights is not None:
+        raise EPBalanceError("grad_weights and pos need weights")
+    if layout is not None:
+        p.layout = ctypes.pointer(layout.c)
+        if layout.num_spare:
+            p.slot_down = _slot_matrix(layout, slot_down, slot_down_scale, I, K, "slot_down")
+    _check(lib().ep_grouped_swiglu_backward(ctypes.byref(p), _stream(stream)), "ep_grouped_swiglu_backward")
+    return grad, q, q_scale, grad_weights
 
 
 def ep_moe_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, out=None, stream=None) -> torch.Tensor:
