@@ -11,6 +11,7 @@ namespace {
 
 struct WholeTile {
     static constexpr int kMatrices = 1;
+    static constexpr bool kLong = false;
     struct Args {
         uint16_t *y;
     };

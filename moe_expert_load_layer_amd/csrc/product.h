@@ -69,9 +69,9 @@ __device__ __forceinline__ int scale_at(int row, int block) {
     return (row * kScaleBlocks | scale_exchange(row)) ^ block;
 }
 
-// this lane's 32 bytes of LDS row r (lanes 0 .. 31 the first half of its 64)
-__device__ __forceinline__ i32x8 read_frag(const uint8_t *tile, int r) {
-    const int c = lane_id() >> 5 << 1;
+// lane's 32 bytes of LDS row r (lanes 0 .. 31 the first half of its 64)
+__device__ __forceinline__ i32x8 read_frag(const uint8_t *tile, int r, int lane) {
+    const int c = lane >> 5 << 1;
     const u32x4 a = *reinterpret_cast<const u32x4 *>(tile + r * kStep + (exchange(r, c) << 4));
     const u32x4 b = *reinterpret_cast<const u32x4 *>(tile + r * kStep + (exchange(r, c + 1) << 4));
     i32x8 f;
@@ -99,11 +99,11 @@ __device__ __forceinline__ constexpr int frag_row(int wn, int i) {
 // leave nothing to wait behind.
 template <int kMatrices, int BM, int BN, int WN, int FM, int FN, int kLoads, int kWaves>
 __device__ __forceinline__ void product_step(const uint8_t *next, uint32_t fill, const uint8_t *(&src)[kLoads],
-                                             int ahead, int xrow, int wn, const uint8_t *xs, const uint8_t *ws,
-                                             int block, const i32x8 (&fx)[FM], i32x8 (&nx)[FM], i32x8 (&fw)[FN],
+                                             int ahead, int xrow, int wn, int lane, const uint8_t *xs,
+                                             const uint8_t *ws, int block, const i32x8 (&fx)[FM], i32x8 (&nx)[FM], i32x8 (&fw)[FN],
                                              const int (&sx)[FM], int (&ns)[FM], int (&sw)[kMatrices],
                                              f32x16 (&acc)[FN][FM]) {
-    const int r = lane_id() & 31;
+    const int r = lane & 31;
     int nsw[kMatrices];
 #pragma unroll
     for (int i = 0; i < kMatrices; i++) nsw[i] = ws[block * 4 + i * kScaleBlocks * 4];
@@ -117,11 +117,11 @@ __device__ __forceinline__ void product_step(const uint8_t *next, uint32_t fill,
         if (i == 0) {
 #pragma unroll
             for (int j = 0; j < FM; j++) {
-                nx[j] = read_frag(next, xrow + j * 32 + r);
+                nx[j] = read_frag(next, xrow + j * 32 + r, lane);
                 ns[j] = xs[scale_at(xrow + r, block) + j * 32 * kScaleBlocks];
             }
         }
-        fw[i] = read_frag(next, BM + frag_row<kMatrices, BN, WN>(wn, i) + r);
+        fw[i] = read_frag(next, BM + frag_row<kMatrices, BN, WN>(wn, i) + r, lane);
 #pragma unroll
         for (int p = i * kLoads / FN; p < (i + 1) * kLoads / FN; p++) {
             load_lds_1k(src[p], fill + p * kWaves * 1024);
@@ -156,7 +156,8 @@ constexpr int waves_a_simd(int BM, int BN, int WM, int WN, int kStages) {
 // kStages: the next step's stage, those in flight, and this step's, whose
 // operands are in registers and which is filled again.
 //
-// Store: kMatrices, Args, Shared<BM, waves along N> in LDS, and
+// Store: kMatrices, kLong (its store needs most registers), Args, Shared<BM, waves
+// along N> in LDS, and
 //   second(B)   the second matrices' SecondArgs, where there are two
 //   locate(A, B, shared, buf, thread, row, place)  for each row of a tile that is found: the output row it
 //               repeats or is, and the row of x (-1: none)
@@ -288,6 +289,21 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
         f32x16 acc[FN][FM];
         i32x8 fx[FM], fx2[FM], fw[FN];
         int sx[FM], sx2[FM], sw[kMatrices];
+        // reads a tile's first step's operands, which lie in the ring at `slot`
+        auto read_first = [&] {
+            const int l = lane_now();
+            const uint8_t *from = stages + slot * kStage, *xs = scales + chunk0 * kChunk;
+#pragma unroll
+            for (int i = 0; i < kMatrices; i++) sw[i] = xs[wscale + i * kScaleBlocks * 4];
+#pragma unroll
+            for (int j = 0; j < FM; j++) {
+                fx[j] = read_frag(from, wm * WM + j * 32 + (l & 31), l);
+                sx[j] = xs[scale_at(wm * WM + (l & 31), 0) + j * 32 * kScaleBlocks];
+            }
+#pragma unroll
+            for (int i = 0; i < FN; i++)
+                fw[i] = read_frag(from, BM + frag_row<kMatrices, BN, WN>(wn, i) + (l & 31), l);
+        };
         // a tile from nothing: fills the ring and reads the first step's operands
         auto begin = [&] {
             const int l = lane_now();
@@ -303,16 +319,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
                 }
             wait_loads_but<(kStages - 1) * kLoads>();
             __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kMatrices; i++) sw[i] = scales[wscale + i * kScaleBlocks * 4];
-#pragma unroll
-            for (int j = 0; j < FM; j++) {
-                fx[j] = read_frag(stages, wm * WM + j * 32 + (l & 31));
-                sx[j] = scales[scale_at(wm * WM + (l & 31), 0) + j * 32 * kScaleBlocks];
-            }
-#pragma unroll
-            for (int i = 0; i < FN; i++)
-                fw[i] = read_frag(stages, BM + frag_row<kMatrices, BN, WN>(wn, i) + (l & 31));
+            read_first();
         };
         begin();
         for (;;) {
@@ -323,6 +330,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
 #pragma unroll
                     for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
             const bool more = at + walk.stride < walk.to;
+            // a long store needs the registers that the loop's addresses would keep
+            const int lane = Store::kLong ? lane_now() : lane_id();
             const int chunks = (A.kb + kScaleBlocks - 1) / kScaleBlocks;
             int ahead = kStep;
             // A step: its operands are in x, c and fw, the next one's (block `block` of
@@ -336,8 +345,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
                 const int after = slot == kStages - 1 ? 0 : slot + 1;
                 const uint8_t *xs = scales + chunk;
                 product_step<kMatrices, BM, BN, WN, FM, FN, kLoads, kWaves>(
-                    stages + after * kStage, ring + slot * kStage, src, ahead, wm * WM, wn, xs, xs + wscale, block, x,
-                    nx, fw, c, nc, sw, acc);
+                    stages + after * kStage, ring + slot * kStage, src, ahead, wm * WM, wn, lane, xs, xs + wscale,
+                    block, x, nx, fw, c, nc, sw, acc);
                 slot = after;
             };
             // Between the steps at which something happens besides, the loop is bare.
@@ -383,6 +392,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
                 wait_loads();
                 __syncthreads();  // every wave's, before the ring is filled again
                 begin();
+            } else if constexpr (Store::kLong) {
+                read_first();  // again: the store needed their registers
             }
         }
         wait_loads();  // those that nobody reads

@@ -8,6 +8,8 @@
 //             as bf16 (for the weight gradient) and in 8 bits (for the input gradient)
 // Both are one product whose tile becomes the outputs before it leaves the
 // registers: neither [g u] nor d is ever written in 16 bits and read again.
+#include <utility>
+
 #include "product.h"
 
 namespace ep {
@@ -64,8 +66,10 @@ __device__ __forceinline__ float other_half_sum(float v) {
     return __builtin_bit_cast(float, t.a) + __builtin_bit_cast(float, t.b);
 }
 
-// |v| for a block's scale: infinity * 0 is NaN, and fmaxf passes over NaN
-__device__ __forceinline__ float finite_max(float m, float v) { return fmaxf(m, fmaf(v, 0.0f, fabsf(v))); }
+// The largest magnitude for a block's scale, in two steps: over all values (NaN is
+// passed over), and, only where that is infinity, over the finite ones alone.
+__device__ __forceinline__ float largest(float m, float a, float b) { return fmaxf(fmaxf(m, fabsf(a)), fabsf(b)); }
+__device__ __forceinline__ float finite(float m, float v) { return fmaxf(m, fmaf(v, 0.0f, fabsf(v))); }  // infinity * 0 is NaN
 
 // The upper halves of two floats, the lowest bit set where anything below is
 // ("round to odd"): rounding these 8 bits of mantissa to the 4 of 8-bit floating
@@ -74,19 +78,42 @@ __device__ __forceinline__ uint32_t odd_pair(float a, float b) {
     uint32_t x = __builtin_bit_cast(uint32_t, a), y = __builtin_bit_cast(uint32_t, b);
     x |= (x & 0xffffu) + 0xffffu;
     y |= (y & 0xffffu) + 0xffffu;
-    return __builtin_amdgcn_perm(y, x, 0x07060302u);
+    uint32_t v = __builtin_amdgcn_perm(y, x, 0x07060302u);
+    asm volatile("" : "+v"(v));  // one register, not the two that it could be made of again
+    return v;
 }
 
-__device__ __forceinline__ uint32_t four_bytes(float a, float b, float c, float d, float inv) {
-    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
+// The largest finite magnitude of odd pairs.  A float's is a little more, but on the
+// same side of every power of two times 1.75, which is what a scale asks.
+template <int kCount>
+__device__ __forceinline__ float largest_finite(const uint32_t (&v)[kCount][8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kCount; i++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) m = finite(finite(m, bf16_lo(v[i][e])), bf16_hi(v[i][e]));
+    return m;
+}
+
+// 8-bit values of floats, or of odd pairs, over a block's scale: the hardware's
+// conversion divides by a power of two, rounds to nearest with ties to even and makes
+// infinities NaN.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t four_bytes(float a, float b, float c, float d, float scale) {
+    const s16x2 v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(s16x2{0, 0}, a, b, scale, false);
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, c, d, scale, true));
+}
+__device__ __forceinline__ uint32_t four_bytes(uint32_t a, uint32_t b, float scale) {
+    const s16x2 v = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(s16x2{0, 0}, __builtin_bit_cast(bf16x2, a), scale, false);
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v, __builtin_bit_cast(bf16x2, b),
+                                                                                 scale, true));
 }
 // of a fragment held in odd pairs, in its memory order
-__device__ __forceinline__ u32x4 odd_to_memory(const uint32_t (&v)[8], float inv) {
+__device__ __forceinline__ u32x4 odd_to_memory(const uint32_t (&v)[8], float scale) {
     u32x4 q;
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-        q[e] = four_bytes(bf16_lo(v[2 * e]), bf16_hi(v[2 * e]), bf16_lo(v[2 * e + 1]), bf16_hi(v[2 * e + 1]), inv);
+    for (int e = 0; e < 4; e++) q[e] = four_bytes(v[2 * e], v[2 * e + 1], scale);
     return bytes_to_memory(q);
 }
 
@@ -95,8 +122,8 @@ __device__ __forceinline__ u32x4 odd_to_memory(const uint32_t (&v)[8], float inv
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // 16 columns of a bf16 row from column n on, of which the row has N
-__device__ __forceinline__ void store_words(uint16_t *row, int n, int N, const Words &w) {
-    if (n + 16 <= N) {
+__device__ __forceinline__ void store_words(bool whole, uint16_t *row, int n, int N, const Words &w) {
+    if (whole || n + 16 <= N) {
         *reinterpret_cast<u32x4_at2 *>(row + n) = w.lo;
         *reinterpret_cast<u32x4_at2 *>(row + n + 8) = w.hi;
     } else {
@@ -107,9 +134,9 @@ __device__ __forceinline__ void store_words(uint16_t *row, int n, int N, const W
         }
     }
 }
-__device__ __forceinline__ Words load_words(const uint16_t *row, int n, int N) {
+__device__ __forceinline__ Words load_words(bool whole, const uint16_t *row, int n, int N) {
     Words w{{0, 0, 0, 0}, {0, 0, 0, 0}};
-    if (n + 16 <= N) {
+    if (whole || n + 16 <= N) {
         w.lo = *reinterpret_cast<const u32x4_at2 *>(row + n);
         w.hi = *reinterpret_cast<const u32x4_at2 *>(row + n + 8);
     } else {
@@ -121,6 +148,29 @@ __device__ __forceinline__ Words load_words(const uint16_t *row, int n, int N) {
     }
     return w;
 }
+
+// Sets what a fragment has past column `end`, counted from its first, to 0, whatever it
+// was (rows without an input: end = 0), so that the steps after it need not mind.
+__device__ __forceinline__ void mask(f32x16 &v, int end, int l) {
+#pragma unroll
+    for (int e = 0; e < 16; e++) v[e] = e / 4 * 8 + e % 4 + (l >> 5) * 4 < end ? v[e] : 0.0f;
+}
+// f(0), f(1) .. f(N - 1) with constants, however long f is: a loop that the compiler
+// leaves rolled would index registers, and so keep the tile's sums in memory.
+template <class F, int... I>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F f) {
+    each(std::make_integer_sequence<int, N>{}, f);
+}
+
+// Keeps what comes before and after apart, so that the registers of one fragment's
+// steps are free before the next one's.  `now`: computed here and not where it is
+// needed, or all that goes into it is kept until then (hundreds of registers).
+__device__ __forceinline__ void next_fragment() { __builtin_amdgcn_sched_barrier(0); }
+__device__ __forceinline__ void now(float &v) { asm volatile("" : "+v"(v)); }
 
 // A row of scale bytes past its blocks, as ep_quant_rows writes it
 __device__ __forceinline__ void pad_scales(uint8_t *row, int blocks, int stride) {
@@ -138,6 +188,15 @@ __device__ __forceinline__ void zero_words(uint16_t *y, int64_t from, int64_t to
     for (int64_t i = from + id; i < to; i += threads) y[i] = 0;
 }
 
+// Whether a tile has all its rows and columns, and every row an input
+template <int BM, class Tile, class S>
+__device__ __forceinline__ bool whole_tile(const Tile &tile, int columns, int N, const S &shared, int buf) {
+    bool whole = tile.m0 + BM <= tile.m1 && tile.n0 + columns <= N;
+#pragma unroll
+    for (int i = 0; i < BM / kWave; i++) whole = whole && shared.full[buf][i];
+    return __builtin_amdgcn_readfirstlane(whole);
+}
+
 // the weight of a tile's row, 1 without weights
 __device__ __forceinline__ float row_weight(const ProductArgs &A, const float *weights, int row, int place) {
     return !weights ? 1.0f : place < 0 ? 0.0f : weights[A.rows ? A.rows[row] : row];
@@ -151,6 +210,7 @@ __device__ __forceinline__ float row_weight(const ProductArgs &A, const float *w
 template <Keep kKeep>
 struct GatedTile {
     static constexpr int kMatrices = 2;
+    static constexpr bool kLong = true;
     struct Args {
         SecondArgs up;
         const float *weights;
@@ -162,6 +222,7 @@ struct GatedTile {
     template <int BM, int kWavesN>
     struct Shared {
         float weight[2][BM];
+        bool full[2][BM / kWave];  // whether every row of 64 has an input
         uint32_t codes[kWavesN][BM];
     };
 
@@ -171,6 +232,60 @@ struct GatedTile {
     __device__ __forceinline__ static void locate(const ProductArgs &A, const Args &B, S &shared, int buf, int thread,
                                                   int row, int place) {
         shared.weight[buf][thread] = row_weight(A, B.weights, row, place);
+        shared.full[buf][thread / kWave] = __all(place >= 0);
+    }
+
+    // where a row of g or u has infinities
+    template <int F>
+    __device__ __forceinline__ static float largest_finite_of(const f32x16 *const (&v)[F]) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < F; i++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) m = finite(m, (*v[i])[e]);
+        return m;
+    }
+    // h of the wave's columns of a row, and the scale bytes that they need by themselves:
+    // of h, and of g and u where those are kept in 8 bits
+    template <int F>
+    __device__ __forceinline__ static uint32_t activate(const f32x16 *const (&g)[F], const f32x16 *const (&u)[F],
+                                                        float weight, uint32_t (&h)[F][8]) {
+        const float inf = __builtin_inff();
+        float th = 0, tg = 0, tu = 0;
+#pragma unroll
+        for (int i = 0; i < F; i++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                next_fragment();
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float a = (*g[i])[4 * q + e];
+                    v[e] = a * sigmoid(a) * (*u[i])[4 * q + e] * weight;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    if constexpr (kKeep == kEight) {
+                        tg = largest(tg, (*g[i])[4 * q + e], (*g[i])[4 * q + e + 1]);
+                        tu = largest(tu, (*u[i])[4 * q + e], (*u[i])[4 * q + e + 1]);
+                    }
+                    th = largest(th, v[e], v[e + 1]);
+                    h[i][2 * q + e / 2] = odd_pair(v[e], v[e + 1]);
+                }
+                now(th);
+                if constexpr (kKeep == kEight) {
+                    now(tg);
+                    now(tu);
+                }
+            }
+        if (__any(th == inf)) th = largest_finite(h);
+        uint32_t code = fp8_scale_code(other_half_max(th));
+        if constexpr (kKeep == kEight) {
+            if (__any(tg == inf)) tg = largest_finite_of(g);
+            if (__any(tu == inf)) tu = largest_finite_of(u);
+            code |= fp8_scale_code(other_half_max(tg)) << 8 | fp8_scale_code(other_half_max(tu)) << 16;
+        }
+        return code;
     }
 
     template <int BM, int BN, int WM, int WN, int FM, int FN, class S>
@@ -179,45 +294,31 @@ struct GatedTile {
                                                  f32x16 (&acc)[FN][FM]) {
         constexpr int F = FN / 2, kWavesN = BN / WN;
         const int b = tile.n0 / kScaleBlock, c0 = tile.n0 + wn * (WN / 2);
-        const bool whole = __builtin_amdgcn_readfirstlane(tile.n0 + kScaleBlock <= A.N);
-        uint32_t held[kKeep != kNone ? F : 1][FM][8];  // h in odd pairs, where g and u are still needed
+        const bool whole = whole_tile<BM>(tile, kScaleBlock, A.N, shared, buf);
+        if (!whole)
+            each<FM>([&](auto J) {
+                constexpr int j = J;
+                const int end = places[wm * WM + j * 32 + (l & 31)] >= 0 ? A.N - c0 : 0;
 #pragma unroll
-        for (int j = 0; j < FM; j++) {
-            const int r = wm * WM + j * 32 + (l & 31);
-            const bool real = places[r] >= 0;
-            const float weight = shared.weight[buf][r];
-            float th = 0, tg = 0, tu = 0;
-#pragma unroll
-            for (int i = 0; i < F; i++) {
-                float h[16];
-#pragma unroll
-                for (int e = 0; e < 16; e++) {
-                    float g = acc[i][j][e], u = acc[F + i][j][e];
-                    if (!real || (!whole && c0 + i * 32 + e / 4 * 8 + (l >> 5) * 4 + e % 4 >= A.N)) g = u = 0.0f;
-                    h[e] = g * sigmoid(g) * u * weight;
-                    if (!real) h[e] = 0.0f;  // whatever its weight
-                    th = finite_max(th, h[e]);
-                    if constexpr (kKeep == kNone) {
-                        acc[i][j][e] = h[e];
-                    } else {
-                        acc[i][j][e] = g;
-                        acc[F + i][j][e] = u;
-                        tg = finite_max(tg, g);
-                        tu = finite_max(tu, u);
-                    }
+                for (int i = 0; i < F; i++) {
+                    mask(acc[i][j], end - i * 32, l);
+                    mask(acc[F + i][j], end - i * 32, l);
                 }
-                if constexpr (kKeep != kNone)
+            });
+        uint32_t held[FM][F][8];  // h in odd pairs
+        each<FM>([&](auto J) {
+            constexpr int j = J;
+            const int r = wm * WM + j * 32 + (l & 31);
+            const float weight = shared.weight[buf][r];
+            const f32x16 *g[F], *u[F];
 #pragma unroll
-                    for (int e = 0; e < 8; e++) held[i][j][e] = odd_pair(h[2 * e], h[2 * e + 1]);
-            }
-            uint32_t code = fp8_scale_code(other_half_max(th));
-            if constexpr (kKeep == kEight)
-                code |= fp8_scale_code(other_half_max(tg)) << 8 | fp8_scale_code(other_half_max(tu)) << 16;
+            for (int i = 0; i < F; i++) g[i] = &acc[i][j], u[i] = &acc[F + i][j];
+            const uint32_t code = activate(g, u, weight, held[j]);
             if (l < 32) shared.codes[wn][r] = code;
-        }
+        });
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < FM; j++) {
+        each<FM>([&](auto J) {
+            constexpr int j = J;
             const int r = wm * WM + j * 32 + (l & 31), m = tile.m0 + r;
             const bool in = m < tile.m1;
             int ch = 0, cg = 0, cu = 0;
@@ -232,17 +333,13 @@ struct GatedTile {
             const int64_t kept = at + (int64_t)m * B.ib * kScaleBlock;  // twice as far apart
 #pragma unroll
             for (int i = 0; i < F; i++) {
-                u32x4 q;
-                if constexpr (kKeep == kNone) {
-                    q = bytes_of(acc[i][j], pow2_of(254 - ch));
-                } else {
-                    q = odd_to_memory(held[i][j], pow2_of(254 - ch));
-                }
+                next_fragment();
+                const u32x4 q = odd_to_memory(held[j][i], pow2_of(ch));
                 if (in) *reinterpret_cast<u32x4 *>(B.h + at + i * 32) = q;
                 if constexpr (kKeep == kEight) {
                     uint8_t *k = static_cast<uint8_t *>(B.kept) + kept + i * 32;
-                    const u32x4 g = bytes_of(acc[i][j], pow2_of(254 - cg));
-                    const u32x4 u = bytes_of(acc[F + i][j], pow2_of(254 - cu));
+                    const u32x4 g = bytes_of(acc[i][j], pow2_of(cg));
+                    const u32x4 u = bytes_of(acc[F + i][j], pow2_of(cu));
                     if (in) {
                         *reinterpret_cast<u32x4 *>(k) = g;
                         *reinterpret_cast<u32x4 *>(k + B.ib * kScaleBlock) = u;
@@ -251,10 +348,11 @@ struct GatedTile {
                 if constexpr (kKeep == kSixteen) {
                     uint16_t *k = static_cast<uint16_t *>(B.kept) + (int64_t)m * 2 * A.N;
                     const int n = c0 + i * 32 + (l >> 5) * 16;
-                    const Words g = words_of(acc[i][j]), u = words_of(acc[F + i][j]);
+                    const Words g = words_of(acc[i][j]),
+                                u = words_of(acc[F + i][j]);
                     if (in) {
-                        store_words(k, n, A.N, g);
-                        store_words(k + A.N, n, A.N, u);
+                        store_words(whole, k, n, A.N, g);
+                        store_words(whole, k + A.N, n, A.N, u);
                     }
                 }
             }
@@ -269,13 +367,13 @@ struct GatedTile {
                     if (b == B.ib - 1) pad_scales(ks, 2 * B.ib, B.ks);
                 }
             }
-        }
+        });
     }
 
-    __device__ __forceinline__ static u32x4 bytes_of(const f32x16 &v, float inv) {
+    __device__ __forceinline__ static u32x4 bytes_of(const f32x16 &v, float scale) {
         u32x4 q;
 #pragma unroll
-        for (int e = 0; e < 4; e++) q[e] = four_bytes(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], inv);
+        for (int e = 0; e < 4; e++) q[e] = four_bytes(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], scale);
         return bytes_to_memory(q);
     }
     __device__ __forceinline__ static Words words_of(const f32x16 &v) {
@@ -304,6 +402,7 @@ struct GatedTile {
 template <Keep kKeep>
 struct GatedBackTile {
     static constexpr int kMatrices = 1;
+    static constexpr bool kLong = true;
     struct Args {
         const float *weights;
         const void *kept;
@@ -316,12 +415,122 @@ struct GatedBackTile {
     template <int BM, int kWavesN>
     struct Shared {
         float weight[2][BM];
+        bool full[2][BM / kWave];
     };
 
     template <class S>
     __device__ __forceinline__ static void locate(const ProductArgs &A, const Args &B, S &shared, int buf, int thread,
                                                   int row, int place) {
         shared.weight[buf][thread] = row_weight(A, B.weights, row, place);
+        shared.full[buf][thread / kWave] = __all(place >= 0);
+    }
+
+    // What was kept of a fragment's row, 16 columns of g and of u as they lie in
+    // memory; zeros without an input.
+    struct Kept {
+        Words g, u;  // 8 bits: the lower halves only
+    };
+    __device__ __forceinline__ static Kept load_kept(const Args &B, int64_t row, int n, int N, int64_t wide, bool real,
+                                                     bool whole) {
+        Kept k{};
+        if constexpr (kKeep == kEight) {
+            const uint8_t *p = static_cast<const uint8_t *>(B.kept) + row * 2 * wide + n;
+            if (real) {
+                k.g.lo = *reinterpret_cast<const u32x4 *>(p);
+                k.u.lo = *reinterpret_cast<const u32x4 *>(p + wide);
+            }
+        } else {
+            const uint16_t *p = static_cast<const uint16_t *>(B.kept) + row * 2 * N;
+            k.g = load_words(whole, p, n, real ? N : 0);
+            k.u = load_words(whole, p + N, n, real ? N : 0);
+        }
+        return k;
+    }
+    __device__ __forceinline__ static void open_bytes(uint32_t w, float scale, float (&v)[4]) {
+        const auto x = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, false);
+        const auto y = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, true);
+        v[0] = x[0], v[1] = x[1], v[2] = y[0], v[3] = y[1];
+    }
+
+    // A row of the wave's block: what its steps share, and what they leave
+    struct Row {
+        int64_t row;
+        bool in, real;
+        float weight, gs, us;  // the scales of what was kept
+        float tg, tu, dot;     // the largest of dg and du, the sum for dw
+    };
+    template <bool kAll, int FN>
+    __device__ __forceinline__ static void differentiate(const Args &B, Row &R, const f32x16 *const (&acc)[FN], int c0,
+                                                         int N, int l, bool whole, uint32_t (&vg)[FN][8],
+                                                         uint32_t (&vu)[FN][8]) {
+        const int64_t wide = (int64_t)B.ib * kScaleBlock;
+        R.tg = R.tu = R.dot = 0.0f;
+        // all of the row's at once, so that they are waited for once, where there are registers
+        constexpr int kAhead = kAll ? FN : 1;
+        Kept kept[kAhead];
+        if constexpr (kAhead > 1)
+#pragma unroll
+            for (int i = 0; i < FN; i++) kept[i] = load_kept(B, R.row, c0 + i * 32 + (l >> 5) * 16, N, wide, R.real, whole);
+#pragma unroll
+        for (int i = 0; i < FN; i++) {
+            next_fragment();
+            const int n = c0 + i * 32 + (l >> 5) * 16;
+            if constexpr (kAhead == 1) kept[0] = load_kept(B, R.row, n, N, wide, R.real, whole);
+            const Kept &k = kept[kAhead == 1 ? 0 : i];
+            u32x4 bg{}, bu{};
+            uint32_t pg[8], pu[8], wg[8], wu[8];
+            if constexpr (kKeep == kEight) {
+                bg = bytes_from_memory(k.g.lo);
+                bu = bytes_from_memory(k.u.lo);
+            } else {
+                words_from_memory(k.g, pg);
+                words_from_memory(k.u, pu);
+            }
+            // 4 values at a time, which is all that the registers of a wave beside its sums are for
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                next_fragment();
+                float g[4], u[4];
+                if constexpr (kKeep == kEight) {
+                    open_bytes(bg[q], R.gs, g);
+                    open_bytes(bu[q], R.us, u);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        g[2 * e] = bf16_lo(pg[2 * q + e]), g[2 * e + 1] = bf16_hi(pg[2 * q + e]);
+                        u[2 * e] = bf16_lo(pu[2 * q + e]), u[2 * e + 1] = bf16_hi(pu[2 * q + e]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float d = (*acc[i])[4 * q + e];
+                    const float s = sigmoid(g[e]), act = g[e] * s, both = d * u[e];
+                    R.dot = fmaf(act, both, R.dot);
+                    g[e] = both * fmaf(act, 1.0f - s, s) * R.weight;
+                    u[e] = d * act * R.weight;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    R.tg = largest(R.tg, g[2 * e], g[2 * e + 1]);
+                    R.tu = largest(R.tu, u[2 * e], u[2 * e + 1]);
+                    vg[i][2 * q + e] = odd_pair(g[2 * e], g[2 * e + 1]);
+                    vu[i][2 * q + e] = odd_pair(u[2 * e], u[2 * e + 1]);
+                    wg[2 * q + e] = pack_bf16(g[2 * e], g[2 * e + 1]);
+                    wu[2 * q + e] = pack_bf16(u[2 * e], u[2 * e + 1]);
+                }
+                now(R.tg);
+                now(R.tu);
+                now(R.dot);
+            }
+            if (B.dgu) {
+                const Words a = words_to_memory(wg), c = words_to_memory(wu);
+                uint16_t *o = B.dgu + R.row * 2 * N;
+                if (R.in) {
+                    store_words(whole, o, n, N, a);
+                    store_words(whole, o + N, n, N, c);
+                }
+            }
+        }
     }
 
     template <int BM, int BN, int WM, int WN, int FM, int FN, class S>
@@ -329,106 +538,63 @@ struct GatedBackTile {
                                                  const int32_t *places, S &shared, int buf, int wm, int wn, int l,
                                                  f32x16 (&acc)[FN][FM]) {
         static_assert(WN == kScaleBlock, "a wave's columns are one block");
-        const int c0 = tile.n0 + wn * WN, b = c0 / kScaleBlock;
+        const int c0 = __builtin_amdgcn_readfirstlane(tile.n0) + wn * WN, b = c0 / kScaleBlock;
         if (b >= B.ib) return;
-        const bool whole = __builtin_amdgcn_readfirstlane(c0 + WN <= A.N);
         const int64_t wide = (int64_t)B.ib * kScaleBlock;
+        const bool whole = whole_tile<BM>(tile, BN, A.N, shared, buf);
+        if (!whole)
+            each<FM>([&](auto J) {
+                constexpr int j = J;
+                const int end = places[wm * WM + j * 32 + (l & 31)] >= 0 ? A.N - c0 : 0;
 #pragma unroll
-        for (int j = 0; j < FM; j++) {
+                for (int i = 0; i < FN; i++) mask(acc[i][j], end - i * 32, l);
+            });
+        constexpr bool kAll = FM == 1 && kKeep == kEight;
+        each<FM>([&](auto J) {
+            constexpr int j = J;
             const int r = wm * WM + j * 32 + (l & 31), m = tile.m0 + r;
-            const bool in = m < tile.m1, real = in && places[r] >= 0;
-            const int64_t row = in ? m : tile.m0;
-            const float weight = shared.weight[buf][r];
-            float gs = 1, us = 1;
+            Row R;
+            R.in = m < tile.m1;
+            R.real = R.in && places[r] >= 0;
+            R.row = R.in ? m : tile.m0;
+            R.weight = shared.weight[buf][r];
+            R.gs = R.us = 1.0f;
             if constexpr (kKeep == kEight) {
-                gs = pow2_of(B.kept_scale[row * B.qs + b]);
-                us = pow2_of(B.kept_scale[row * B.qs + B.ib + b]);
+                R.gs = pow2_of(B.kept_scale[R.row * B.qs + b]);
+                R.us = pow2_of(B.kept_scale[R.row * B.qs + B.ib + b]);
             }
+            const f32x16 *d[FN];
+#pragma unroll
+            for (int i = 0; i < FN; i++) d[i] = &acc[i][j];
             uint32_t vg[FN][8], vu[FN][8];
-            float tg = 0, tu = 0, dot = 0;
-#pragma unroll
-            for (int i = 0; i < FN; i++) {
-                const int n = c0 + i * 32 + (l >> 5) * 16;
-                float g[16], u[16];
-                if constexpr (kKeep == kEight) {
-                    const uint8_t *k = static_cast<const uint8_t *>(B.kept) + row * 2 * wide + n;
-                    const u32x4 a = bytes_from_memory(*reinterpret_cast<const u32x4 *>(k));
-                    const u32x4 c = bytes_from_memory(*reinterpret_cast<const u32x4 *>(k + wide));
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const auto g0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a[e], false);
-                        const auto g1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a[e], true);
-                        const auto u0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[e], false);
-                        const auto u1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[e], true);
-                        g[4 * e] = g0[0] * gs, g[4 * e + 1] = g0[1] * gs, g[4 * e + 2] = g1[0] * gs, g[4 * e + 3] = g1[1] * gs;
-                        u[4 * e] = u0[0] * us, u[4 * e + 1] = u0[1] * us, u[4 * e + 2] = u1[0] * us, u[4 * e + 3] = u1[1] * us;
-                    }
-                } else {
-                    const uint16_t *k = static_cast<const uint16_t *>(B.kept) + row * 2 * A.N;
-                    uint32_t a[8], c[8];
-                    words_from_memory(load_words(k, n, A.N), a);
-                    words_from_memory(load_words(k + A.N, n, A.N), c);
-#pragma unroll
-                    for (int e = 0; e < 8; e++) {
-                        g[2 * e] = bf16_lo(a[e]), g[2 * e + 1] = bf16_hi(a[e]);
-                        u[2 * e] = bf16_lo(c[e]), u[2 * e + 1] = bf16_hi(c[e]);
-                    }
-                }
-                float dg[16], du[16];
-#pragma unroll
-                for (int e = 0; e < 16; e++) {
-                    const float d = acc[i][j][e], s = sigmoid(g[e]), act = g[e] * s, dw = d * weight;
-                    float x = dw * u[e] * (s * (1.0f + g[e] * (1.0f - s))), y = dw * act, z = d * (act * u[e]);
-                    if (!real || (!whole && c0 + i * 32 + e / 4 * 8 + (l >> 5) * 4 + e % 4 >= A.N)) x = y = z = 0.0f;
-                    dg[e] = x;
-                    du[e] = y;
-                    dot += z;
-                    tg = finite_max(tg, x);
-                    tu = finite_max(tu, y);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    vg[i][e] = odd_pair(dg[2 * e], dg[2 * e + 1]);
-                    vu[i][e] = odd_pair(du[2 * e], du[2 * e + 1]);
-                }
-                if (B.dgu) {
-                    uint32_t wg[8], wu[8];
-#pragma unroll
-                    for (int e = 0; e < 8; e++) {
-                        wg[e] = pack_bf16(dg[2 * e], dg[2 * e + 1]);
-                        wu[e] = pack_bf16(du[2 * e], du[2 * e + 1]);
-                    }
-                    const Words a = words_to_memory(wg), c = words_to_memory(wu);
-                    uint16_t *o = B.dgu + row * 2 * A.N;
-                    if (in) {
-                        store_words(o, n, A.N, a);
-                        store_words(o + A.N, n, A.N, c);
-                    }
-                }
-            }
+            differentiate<kAll>(B, R, d, c0, A.N, l, whole, vg, vu);
             if (B.q) {
-                const int cg = fp8_scale_code(other_half_max(tg)), cu = fp8_scale_code(other_half_max(tu));
-                uint8_t *q = B.q + row * 2 * wide + c0 + (l >> 5) * 16;
+                const float inf = __builtin_inff();
+                if (__any(R.tg == inf)) R.tg = largest_finite(vg);
+                if (__any(R.tu == inf)) R.tu = largest_finite(vu);
+                const int cg = fp8_scale_code(other_half_max(R.tg)), cu = fp8_scale_code(other_half_max(R.tu));
+                uint8_t *q = B.q + R.row * 2 * wide + c0 + (l >> 5) * 16;
 #pragma unroll
                 for (int i = 0; i < FN; i++) {
-                    const u32x4 a = odd_to_memory(vg[i], pow2_of(254 - cg)), c = odd_to_memory(vu[i], pow2_of(254 - cu));
-                    if (in) {
+                    next_fragment();
+                    const u32x4 a = odd_to_memory(vg[i], pow2_of(cg)), c = odd_to_memory(vu[i], pow2_of(cu));
+                    if (R.in) {
                         *reinterpret_cast<u32x4 *>(q + i * 32) = a;
                         *reinterpret_cast<u32x4 *>(q + wide + i * 32) = c;
                     }
                 }
-                if (in && l < 32) {
-                    uint8_t *s = B.q_scale + row * B.qs;
+                if (R.in && l < 32) {
+                    uint8_t *s = B.q_scale + R.row * B.qs;
                     s[b] = (uint8_t)cg;
                     s[B.ib + b] = (uint8_t)cu;
                     if (b == B.ib - 1) pad_scales(s, 2 * B.ib, B.qs);
                 }
             }
             if (B.dots) {
-                const float sum = other_half_sum(dot);
-                if (in && l < 32) B.dots[row * B.ib + b] = sum;
+                const float sum = other_half_sum(R.dot);
+                if (R.in && l < 32) B.dots[R.row * B.ib + b] = sum;
             }
-        }
+        });
     }
 
     // rows of zeros
@@ -474,7 +640,7 @@ hipError_t backward(const ProductArgs &A, const typename GatedBackTile<kEight>::
     const typename Tile::Args C{B.weights, B.kept, B.kept_scale, B.dgu, B.q, B.q_scale, B.dots, B.ib, B.qs};
     const int64_t rows = A.groups.M / A.groups.G;
     auto enough = [&](int64_t tile) { return ceil_div(A.groups.M, tile) * ceil_div(A.N, tile) >= 192; };
-    if (rows >= 256 && enough(256)) return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
+    if (rows >= 256 && enough(256)) return launch_product<Tile, 128, 256, 32, 128, 4>(A, C, s);
     if (rows >= 96) return launch_product<Tile, 128, 128, 32, 128, 4>(A, C, s);
     return launch_product<Tile, 64, 128, 32, 128, 6>(A, C, s);
 }

@@ -3,12 +3,14 @@ the kernels may differ by.  Definitions only, no code of the package.
 
 Products in 8 bits: 7 2^-13 sum |x w| (7 dropped rests below 2^-13 of the largest of each 8 products).  The sigmoid
 through the hardware's exponential and reciprocal: the exponent is off by 2^-24 |g| log2 e, the two steps by an ulp
-each, together below 2^-16 of a value for |g| <= 128.  What is rounded afterwards is checked by the rounding's
+each, together below 2^-16 of a value for |g| <= 128; and it gives 0 for results below the least normal float, 2^-126,
+which sigmoid(g) is from g = -87.4 on: there it is off by all of itself, less than 2^-126 (TINY).  What is rounded afterwards is checked by the rounding's
 monotony: the output lies between the roundings of value - bound and value + bound."""
 import torch
 
 DROPPED = 7 * 2.0 ** -13
 HARDWARE = 2.0 ** -16
+TINY = 2.0 ** -126
 
 
 def _levels(device):
@@ -83,7 +85,7 @@ def forward(x, gate, up, weights):
     s = torch.sigmoid(g)
     a = g * s
     h = a * u * weights
-    ea = 1.1 * eg + a.abs() * HARDWARE         # |silu'| < 1.1
+    ea = 1.1 * eg + a.abs() * HARDWARE + g.abs() * TINY    # |silu'| < 1.1
     eh = weights.abs() * (ea * u.abs() + a.abs() * eu + ea * eu) + h.abs() * 2.0 ** -22
     return g, eg, u, eu, h, eh
 
@@ -92,9 +94,11 @@ def backward(d, ed, g, u, weights):
     """Rows of d known to ed -> dg, du, the terms of dw, each with its bound."""
     s = torch.sigmoid(g)
     slope, a = s * (1 + g * (1 - s)), g * s
-    eslope = 2 * HARDWARE * s * (1 + g.abs())  # of s, in both of its places
+    es = HARDWARE * s + TINY
+    eslope = 2 * es * (1 + g.abs())            # of s, in both of its places
     dg, du, dw = weights * d * u * slope, weights * d * a, d * a * u
     edg = (weights * u).abs() * (slope.abs() * ed + (d.abs() + ed) * eslope) + dg.abs() * 2.0 ** -21
-    edu = weights.abs() * a.abs() * (ed + (d.abs() + ed) * HARDWARE) + du.abs() * 2.0 ** -21
-    edw = (a * u).abs() * (ed + (d.abs() + ed) * HARDWARE) + dw.abs() * 2.0 ** -21
+    ea = g.abs() * es
+    edu = weights.abs() * (a.abs() * ed + (d.abs() + ed) * ea) + du.abs() * 2.0 ** -21
+    edw = u.abs() * (a.abs() * ed + (d.abs() + ed) * ea) + dw.abs() * 2.0 ** -21
     return dg, edg, du, edu, dw, edw

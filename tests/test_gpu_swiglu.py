@@ -121,7 +121,8 @@ SHAPES = [
     ([1, 1, 1, 1], 768, 256, 4, True, 0, True), ([100, 130], 513, 255, 0, False, 3, True),
     ([200, 97, 128], 700, 640, 8, True, 0, True), ([128, 300], 2048, 384, 0, False, 0, True),
     ([4100], 200, 1500, 4, True, 0, True), ([2500, 1700, 0], 650, 1800, 8, False, 90, True),
-    ([5000], 1024, 1280, 0, False, 0, False),
+    ([5000], 1024, 1280, 0, False, 0, False), ([30000, 22000, 0], 99, 103, 8, False, 0, True),
+    ([26000, 30001], 640, 130, 4, True, 5, True),
 ]
 
 
