@@ -19,8 +19,13 @@ enum Keep { kNone, kSixteen, kEight };
 
 // ---- a lane's 16 values of a 32 x 32 fragment ----
 // Value e belongs to column 8 (e / 4) + 4 (lane / 32) + e % 4 of the fragment's
-// row lane % 32.  Memory wants 16 consecutive columns a lane, the lower lanes
-// the first ones: a swap between the halves of the wave goes either way.
+// row lane % 32.  Memory takes rows in pieces of 64 bytes best, 16 from each of 4
+// lanes (pieces of 32 cost twice the requests: the backward kernel's stores took
+// NEW), so two swaps bring them together:
+//   between the halves of the wave, after which a lane has 16 bytes in a row;
+//   between rows of 16 lanes, of two such vectors that lie side by side in memory: one
+//   then has both of rows 0 .. 15 of the fragment, the other both of rows 16 .. 31.
+// Each swap undoes itself, so that the same way leads back.
 
 struct Two {
     uint32_t a, b;
@@ -28,6 +33,18 @@ struct Two {
 __device__ __forceinline__ Two swap_halves(uint32_t a, uint32_t b) {
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
     return Two{r[0], r[1]};
+}
+struct Pair {
+    u32x4 lo, hi;  // 16 bytes and the 16 or 32 that follow; or rows 0 .. 15 and 16 .. 31
+};
+__device__ __forceinline__ Pair swap_rows(const Pair &p) {
+    Pair r;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const auto t = __builtin_amdgcn_permlane16_swap(p.lo[i], p.hi[i], false, false);
+        r.lo[i] = t[0], r.hi[i] = t[1];
+    }
+    return r;
 }
 
 // four bytes for every 4 values, to and from 16 consecutive bytes
@@ -39,21 +56,23 @@ __device__ __forceinline__ u32x4 bytes_from_memory(const u32x4 &v) {
     const Two p = swap_halves(v[0], v[1]), q = swap_halves(v[2], v[3]);
     return u32x4{p.a, q.a, p.b, q.b};
 }
-
-struct Words {
-    u32x4 lo, hi;  // 8 columns each
-};
-// the same for 16-bit values, two a word
-__device__ __forceinline__ Words words_to_memory(const uint32_t (&v)[8]) {
-    const Two a = swap_halves(v[0], v[4]), b = swap_halves(v[1], v[5]), c = swap_halves(v[2], v[6]),
-              d = swap_halves(v[3], v[7]);
-    return Words{u32x4{a.a, b.a, a.b, b.b}, u32x4{c.a, d.a, c.b, d.b}};
+// 16-bit values, two a word: 8 columns and the 8 that lie 16 further on
+__device__ __forceinline__ Pair words_to_memory(const uint32_t (&v)[8]) {
+    const Two a = swap_halves(v[0], v[2]), b = swap_halves(v[1], v[3]), c = swap_halves(v[4], v[6]),
+              d = swap_halves(v[5], v[7]);
+    return Pair{u32x4{a.a, b.a, a.b, b.b}, u32x4{c.a, d.a, c.b, d.b}};
 }
-__device__ __forceinline__ void words_from_memory(const Words &w, uint32_t (&v)[8]) {
+__device__ __forceinline__ void words_from_memory(const Pair &w, uint32_t (&v)[8]) {
     const Two a = swap_halves(w.lo[0], w.lo[2]), b = swap_halves(w.lo[1], w.lo[3]), c = swap_halves(w.hi[0], w.hi[2]),
               d = swap_halves(w.hi[1], w.hi[3]);
-    v[0] = a.a, v[4] = a.b, v[1] = b.a, v[5] = b.b, v[2] = c.a, v[6] = c.b, v[3] = d.a, v[7] = d.b;
+    v[0] = a.a, v[2] = a.b, v[1] = b.a, v[3] = b.b, v[4] = c.a, v[6] = c.b, v[5] = d.a, v[7] = d.b;
 }
+// Where a lane's 16 bytes lie once rows are swapped: its row of a Pair's first half (the
+// second's is 16 further), its byte of two fragments' 64 in 8 bits, its column of a
+// fragment's 32 in 16
+__device__ __forceinline__ int piece_row(int l) { return l & 15; }
+__device__ __forceinline__ int piece_byte(int l) { return (l >> 4 & 1) * 32 + (l >> 5) * 16; }
+__device__ __forceinline__ int piece_column(int l) { return (l >> 4 & 1) * 16 + (l >> 5) * 8; }
 
 __device__ __forceinline__ float other_half_max(float v) {
     const uint32_t b = __builtin_bit_cast(uint32_t, v);
@@ -71,20 +90,19 @@ __device__ __forceinline__ float other_half_sum(float v) {
 __device__ __forceinline__ float largest(float m, float a, float b) { return fmaxf(fmaxf(m, fabsf(a)), fabsf(b)); }
 __device__ __forceinline__ float finite(float m, float v) { return fmaxf(m, fmaf(v, 0.0f, fabsf(v))); }  // infinity * 0 is NaN
 
-// The upper halves of two floats, the lowest bit set where anything below is
-// ("round to odd"): rounding these 8 bits of mantissa to the 4 of 8-bit floating
-// point then gives what rounding the floats themselves does, bit for bit.
+// The upper halves of two floats with the lowest bit set: rounding these 8 bits of
+// mantissa to the 4 of 8-bit floating point then gives what rounding the floats
+// themselves does, but for ties, which go away from zero.  (A bit set only where
+// something was below it would take three more instructions a value, a sixth of the
+// backward kernel's, for cases that the sums' own error decides.)
 __device__ __forceinline__ uint32_t odd_pair(float a, float b) {
-    uint32_t x = __builtin_bit_cast(uint32_t, a), y = __builtin_bit_cast(uint32_t, b);
-    x |= (x & 0xffffu) + 0xffffu;
-    y |= (y & 0xffffu) + 0xffffu;
-    uint32_t v = __builtin_amdgcn_perm(y, x, 0x07060302u);
+    uint32_t v = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u) |
+                 0x00010001u;
     asm volatile("" : "+v"(v));  // one register, not the two that it could be made of again
     return v;
 }
 
-// The largest finite magnitude of odd pairs.  A float's is a little more, but on the
-// same side of every power of two times 1.75, which is what a scale asks.
+// The largest finite magnitude of odd pairs, for rows that hold infinities.
 template <int kCount>
 __device__ __forceinline__ float largest_finite(const uint32_t (&v)[kCount][8]) {
     float m = 0.0f;
@@ -100,6 +118,18 @@ __device__ __forceinline__ float largest_finite(const uint32_t (&v)[kCount][8]) 
 // infinities NaN.
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// Where a block's scale is next to the least (of blocks of zeros, it is), the set bits
+// would not vanish below its steps: they are taken away again.
+template <int kCount>
+__device__ __forceinline__ void settle(uint32_t (&v)[kCount][8], int code) {
+    if (!__any(code <= 8)) return;
+    const uint32_t kept = code <= 8 ? 0xfffefffeu : 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < kCount; i++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) v[i][e] &= kept;
+}
+
 __device__ __forceinline__ uint32_t four_bytes(float a, float b, float c, float d, float scale) {
     const s16x2 v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(s16x2{0, 0}, a, b, scale, false);
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, c, d, scale, true));
@@ -121,30 +151,24 @@ __device__ __forceinline__ u32x4 odd_to_memory(const uint32_t (&v)[8], float sca
 // most, against the 2^-4 (8 bits) or 2^-9 (bf16) of the roundings that follow.
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
-// 16 columns of a bf16 row from column n on, of which the row has N
-__device__ __forceinline__ void store_words(bool whole, uint16_t *row, int n, int N, const Words &w) {
-    if (whole || n + 16 <= N) {
-        *reinterpret_cast<u32x4_at2 *>(row + n) = w.lo;
-        *reinterpret_cast<u32x4_at2 *>(row + n + 8) = w.hi;
+// Columns n .. n + 7 of a bf16 row of N
+__device__ __forceinline__ void store_words(bool whole, uint16_t *row, int n, int N, const u32x4 &w) {
+    if (whole || n + 8 <= N) {
+        *reinterpret_cast<u32x4_at2 *>(row + n) = w;
     } else {
 #pragma unroll
-        for (int q = 0; q < 16; q++) {
-            const u32x4 &v = q < 8 ? w.lo : w.hi;
-            if (n + q < N) row[n + q] = (uint16_t)(v[q % 8 / 2] >> (16 * (q % 2)));
-        }
+        for (int q = 0; q < 8; q++)
+            if (n + q < N) row[n + q] = (uint16_t)(w[q / 2] >> (16 * (q % 2)));
     }
 }
-__device__ __forceinline__ Words load_words(bool whole, const uint16_t *row, int n, int N) {
-    Words w{{0, 0, 0, 0}, {0, 0, 0, 0}};
-    if (whole || n + 16 <= N) {
-        w.lo = *reinterpret_cast<const u32x4_at2 *>(row + n);
-        w.hi = *reinterpret_cast<const u32x4_at2 *>(row + n + 8);
+__device__ __forceinline__ u32x4 load_words(bool whole, const uint16_t *row, int n, int N) {
+    u32x4 w{0, 0, 0, 0};
+    if (whole || n + 8 <= N) {
+        w = *reinterpret_cast<const u32x4_at2 *>(row + n);
     } else {
 #pragma unroll
-        for (int q = 0; q < 16; q++) {
-            u32x4 &v = q < 8 ? w.lo : w.hi;
-            if (n + q < N) v[q % 8 / 2] |= (uint32_t)row[n + q] << (16 * (q % 2));
-        }
+        for (int q = 0; q < 8; q++)
+            if (n + q < N) w[q / 2] |= (uint32_t)row[n + q] << (16 * (q % 2));
     }
     return w;
 }
@@ -329,32 +353,55 @@ struct GatedTile {
                 cg = max(cg, (int)(code >> 8 & 255));
                 cu = max(cu, (int)(code >> 16));
             }
-            const int64_t at = (int64_t)m * B.ib * kScaleBlock + c0 + (l >> 5) * 16;
-            const int64_t kept = at + (int64_t)m * B.ib * kScaleBlock;  // twice as far apart
+            settle(held[j], ch);
+            // rows of 16 lanes' pieces, and whether they are the group's
+            const int m0 = tile.m0 + wm * WM + j * 32 + piece_row(l);
+            const bool in0 = m0 < tile.m1, in1 = m0 + 16 < tile.m1;
+            const int wide = B.ib * kScaleBlock;
+            constexpr int kSide = F % 2 == 0 ? 2 : 1;  // fragments side by side in 8 bits
+            // 8-bit rows `stride` bytes apart, two fragments or one
+            auto put = [&](uint8_t *to, int stride, const u32x4 (&v)[kSide], int i) {
+                if constexpr (kSide == 2) {
+                    const Pair p = swap_rows(Pair{v[0], v[1]});
+                    uint8_t *o = to + (int64_t)m0 * stride + c0 + i * 32 + piece_byte(l);
+                    if (in0) *reinterpret_cast<u32x4 *>(o) = p.lo;
+                    if (in1) *reinterpret_cast<u32x4 *>(o + (int64_t)16 * stride) = p.hi;
+                } else {
+                    if (in) *reinterpret_cast<u32x4 *>(to + (int64_t)m * stride + c0 + i * 32 + (l >> 5) * 16) = v[0];
+                }
+            };
 #pragma unroll
-            for (int i = 0; i < F; i++) {
+            for (int i = 0; i < F; i += kSide) {
                 next_fragment();
-                const u32x4 q = odd_to_memory(held[j][i], pow2_of(ch));
-                if (in) *reinterpret_cast<u32x4 *>(B.h + at + i * 32) = q;
+                u32x4 v[kSide];
+#pragma unroll
+                for (int k = 0; k < kSide; k++) v[k] = odd_to_memory(held[j][i + k], pow2_of(ch));
+                put(B.h, wide, v, i);
                 if constexpr (kKeep == kEight) {
-                    uint8_t *k = static_cast<uint8_t *>(B.kept) + kept + i * 32;
-                    const u32x4 g = bytes_of(acc[i][j], pow2_of(cg));
-                    const u32x4 u = bytes_of(acc[F + i][j], pow2_of(cu));
-                    if (in) {
-                        *reinterpret_cast<u32x4 *>(k) = g;
-                        *reinterpret_cast<u32x4 *>(k + B.ib * kScaleBlock) = u;
-                    }
+                    uint8_t *kept = static_cast<uint8_t *>(B.kept);
+#pragma unroll
+                    for (int k = 0; k < kSide; k++) v[k] = bytes_of(acc[i + k][j], pow2_of(cg));
+                    put(kept, 2 * wide, v, i);
+#pragma unroll
+                    for (int k = 0; k < kSide; k++) v[k] = bytes_of(acc[F + i + k][j], pow2_of(cu));
+                    put(kept + wide, 2 * wide, v, i);
                 }
-                if constexpr (kKeep == kSixteen) {
-                    uint16_t *k = static_cast<uint16_t *>(B.kept) + (int64_t)m * 2 * A.N;
-                    const int n = c0 + i * 32 + (l >> 5) * 16;
-                    const Words g = words_of(acc[i][j]),
-                                u = words_of(acc[F + i][j]);
-                    if (in) {
-                        store_words(whole, k, n, A.N, g);
-                        store_words(whole, k + A.N, n, A.N, u);
+                if constexpr (kKeep == kSixteen)
+#pragma unroll
+                    for (int k = 0; k < kSide; k++) {
+                        uint16_t *kept = static_cast<uint16_t *>(B.kept) + (int64_t)m0 * 2 * A.N;
+                        const int64_t down = (int64_t)16 * 2 * A.N;
+                        const int n = c0 + (i + k) * 32 + piece_column(l);
+                        const Pair g = swap_rows(words_of(acc[i + k][j])), u = swap_rows(words_of(acc[F + i + k][j]));
+                        if (in0) {
+                            store_words(whole, kept, n, A.N, g.lo);
+                            store_words(whole, kept + A.N, n, A.N, u.lo);
+                        }
+                        if (in1) {
+                            store_words(whole, kept + down, n, A.N, g.hi);
+                            store_words(whole, kept + down + A.N, n, A.N, u.hi);
+                        }
                     }
-                }
             }
             if (in && wn == 0 && l < 32) {
                 uint8_t *hs = B.h_scale + (int64_t)m * B.hs;
@@ -376,7 +423,7 @@ struct GatedTile {
         for (int e = 0; e < 4; e++) q[e] = four_bytes(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], scale);
         return bytes_to_memory(q);
     }
-    __device__ __forceinline__ static Words words_of(const f32x16 &v) {
+    __device__ __forceinline__ static Pair words_of(const f32x16 &v) {
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
@@ -425,25 +472,42 @@ struct GatedBackTile {
         shared.full[buf][thread / kWave] = __all(place >= 0);
     }
 
-    // What was kept of a fragment's row, 16 columns of g and of u as they lie in
-    // memory; zeros without an input.
+    // What was kept of two fragments' rows (8 bits) or of one's (bf16), as it lies in
+    // memory.  Rows without an input are rows of zeros there.
+    static constexpr int kSide = kKeep == kEight ? 2 : 1;
     struct Kept {
-        Words g, u;  // 8 bits: the lower halves only
+        Pair g, u;
     };
-    __device__ __forceinline__ static Kept load_kept(const Args &B, int64_t row, int n, int N, int64_t wide, bool real,
-                                                     bool whole) {
+    // A wave's 32 rows: the place of a lane's pieces
+    struct Rows {
+        int64_t row;    // of the first piece; the second's is 16 further
+        bool in0, in1;  // whether they are the group's
+        bool whole;     // and all columns are there
+    };
+    __device__ __forceinline__ static Kept load_kept(const Args &B, const Rows &R, int n, int N, int l) {
         Kept k{};
         if constexpr (kKeep == kEight) {
-            const uint8_t *p = static_cast<const uint8_t *>(B.kept) + row * 2 * wide + n;
-            if (real) {
+            const int64_t wide = (int64_t)B.ib * kScaleBlock;
+            const uint8_t *p = static_cast<const uint8_t *>(B.kept) + R.row * 2 * wide + n + piece_byte(l);
+            if (R.in0) {
                 k.g.lo = *reinterpret_cast<const u32x4 *>(p);
                 k.u.lo = *reinterpret_cast<const u32x4 *>(p + wide);
             }
+            if (R.in1) {
+                k.g.hi = *reinterpret_cast<const u32x4 *>(p + 32 * wide);
+                k.u.hi = *reinterpret_cast<const u32x4 *>(p + 33 * wide);
+            }
         } else {
-            const uint16_t *p = static_cast<const uint16_t *>(B.kept) + row * 2 * N;
-            k.g = load_words(whole, p, n, real ? N : 0);
-            k.u = load_words(whole, p + N, n, real ? N : 0);
+            const uint16_t *p = static_cast<const uint16_t *>(B.kept) + R.row * 2 * N;
+            const int64_t down = (int64_t)32 * N;
+            n += piece_column(l);
+            k.g.lo = load_words(R.whole, p, n, R.in0 ? N : 0);
+            k.u.lo = load_words(R.whole, p + N, n, R.in0 ? N : 0);
+            k.g.hi = load_words(R.whole, p + down, n, R.in1 ? N : 0);
+            k.u.hi = load_words(R.whole, p + down + N, n, R.in1 ? N : 0);
         }
+        k.g = swap_rows(k.g);
+        k.u = swap_rows(k.u);
         return k;
     }
     __device__ __forceinline__ static void open_bytes(uint32_t w, float scale, float (&v)[4]) {
@@ -452,39 +516,33 @@ struct GatedBackTile {
         v[0] = x[0], v[1] = x[1], v[2] = y[0], v[3] = y[1];
     }
 
-    // A row of the wave's block: what its steps share, and what they leave
+    // A lane's row of the wave's block: what its steps share, and what they leave
     struct Row {
-        int64_t row;
-        bool in, real;
         float weight, gs, us;  // the scales of what was kept
         float tg, tu, dot;     // the largest of dg and du, the sum for dw
     };
-    template <bool kAll, int FN>
-    __device__ __forceinline__ static void differentiate(const Args &B, Row &R, const f32x16 *const (&acc)[FN], int c0,
-                                                         int N, int l, bool whole, uint32_t (&vg)[FN][8],
-                                                         uint32_t (&vu)[FN][8]) {
-        const int64_t wide = (int64_t)B.ib * kScaleBlock;
+    template <int FN>
+    __device__ __forceinline__ static void differentiate(const Args &B, const Rows &W, Row &R,
+                                                         const f32x16 *const (&acc)[FN], int c0, int N, int l,
+                                                         uint32_t (&vg)[FN][8], uint32_t (&vu)[FN][8]) {
         R.tg = R.tu = R.dot = 0.0f;
-        // all of the row's at once, so that they are waited for once, where there are registers
-        constexpr int kAhead = kAll ? FN : 1;
-        Kept kept[kAhead];
-        if constexpr (kAhead > 1)
-#pragma unroll
-            for (int i = 0; i < FN; i++) kept[i] = load_kept(B, R.row, c0 + i * 32 + (l >> 5) * 16, N, wide, R.real, whole);
+        // a fragment's are on their way while the one before is computed
+        Kept now_kept{}, next = load_kept(B, W, c0, N, l);
 #pragma unroll
         for (int i = 0; i < FN; i++) {
             next_fragment();
-            const int n = c0 + i * 32 + (l >> 5) * 16;
-            if constexpr (kAhead == 1) kept[0] = load_kept(B, R.row, n, N, wide, R.real, whole);
-            const Kept &k = kept[kAhead == 1 ? 0 : i];
+            if (i % kSide == 0) {
+                now_kept = next;
+                if (i + kSide < FN) next = load_kept(B, W, c0 + (i + kSide) * 32, N, l);
+            }
             u32x4 bg{}, bu{};
             uint32_t pg[8], pu[8], wg[8], wu[8];
             if constexpr (kKeep == kEight) {
-                bg = bytes_from_memory(k.g.lo);
-                bu = bytes_from_memory(k.u.lo);
+                bg = bytes_from_memory(i % 2 ? now_kept.g.hi : now_kept.g.lo);
+                bu = bytes_from_memory(i % 2 ? now_kept.u.hi : now_kept.u.lo);
             } else {
-                words_from_memory(k.g, pg);
-                words_from_memory(k.u, pu);
+                words_from_memory(now_kept.g, pg);
+                words_from_memory(now_kept.u, pu);
             }
             // 4 values at a time, which is all that the registers of a wave beside its sums are for
 #pragma unroll
@@ -523,11 +581,17 @@ struct GatedBackTile {
                 now(R.dot);
             }
             if (B.dgu) {
-                const Words a = words_to_memory(wg), c = words_to_memory(wu);
-                uint16_t *o = B.dgu + R.row * 2 * N;
-                if (R.in) {
-                    store_words(whole, o, n, N, a);
-                    store_words(whole, o + N, n, N, c);
+                const Pair g = swap_rows(words_to_memory(wg)), u = swap_rows(words_to_memory(wu));
+                uint16_t *o = B.dgu + W.row * 2 * N;
+                const int64_t down = (int64_t)32 * N;
+                const int n = c0 + i * 32 + piece_column(l);
+                if (W.in0) {
+                    store_words(W.whole, o, n, N, g.lo);
+                    store_words(W.whole, o + N, n, N, u.lo);
+                }
+                if (W.in1) {
+                    store_words(W.whole, o + down, n, N, g.hi);
+                    store_words(W.whole, o + down + N, n, N, u.hi);
                 }
             }
         }
@@ -549,42 +613,49 @@ struct GatedBackTile {
 #pragma unroll
                 for (int i = 0; i < FN; i++) mask(acc[i][j], end - i * 32, l);
             });
-        constexpr bool kAll = FM == 1 && kKeep == kEight;
         each<FM>([&](auto J) {
             constexpr int j = J;
             const int r = wm * WM + j * 32 + (l & 31), m = tile.m0 + r;
+            const int m0 = tile.m0 + wm * WM + j * 32 + piece_row(l);
+            const Rows W{m0, m0 < tile.m1, m0 + 16 < tile.m1, whole};
+            const bool in = m < tile.m1;
+            const int64_t row = in ? m : tile.m0;
             Row R;
-            R.in = m < tile.m1;
-            R.real = R.in && places[r] >= 0;
-            R.row = R.in ? m : tile.m0;
             R.weight = shared.weight[buf][r];
             R.gs = R.us = 1.0f;
             if constexpr (kKeep == kEight) {
-                R.gs = pow2_of(B.kept_scale[R.row * B.qs + b]);
-                R.us = pow2_of(B.kept_scale[R.row * B.qs + B.ib + b]);
+                R.gs = pow2_of(B.kept_scale[row * B.qs + b]);
+                R.us = pow2_of(B.kept_scale[row * B.qs + B.ib + b]);
             }
             const f32x16 *d[FN];
 #pragma unroll
             for (int i = 0; i < FN; i++) d[i] = &acc[i][j];
             uint32_t vg[FN][8], vu[FN][8];
-            differentiate<kAll>(B, R, d, c0, A.N, l, whole, vg, vu);
+            differentiate(B, W, R, d, c0, A.N, l, vg, vu);
             if (B.q) {
                 const float inf = __builtin_inff();
                 if (__any(R.tg == inf)) R.tg = largest_finite(vg);
                 if (__any(R.tu == inf)) R.tu = largest_finite(vu);
                 const int cg = fp8_scale_code(other_half_max(R.tg)), cu = fp8_scale_code(other_half_max(R.tu));
-                uint8_t *q = B.q + R.row * 2 * wide + c0 + (l >> 5) * 16;
+                settle(vg, cg);
+                settle(vu, cu);
+                uint8_t *q = B.q + W.row * 2 * wide + c0 + piece_byte(l);
 #pragma unroll
-                for (int i = 0; i < FN; i++) {
+                for (int i = 0; i < FN; i += 2) {
                     next_fragment();
-                    const u32x4 a = odd_to_memory(vg[i], pow2_of(cg)), c = odd_to_memory(vu[i], pow2_of(cu));
-                    if (R.in) {
-                        *reinterpret_cast<u32x4 *>(q + i * 32) = a;
-                        *reinterpret_cast<u32x4 *>(q + wide + i * 32) = c;
+                    const Pair g = swap_rows(Pair{odd_to_memory(vg[i], pow2_of(cg)), odd_to_memory(vg[i + 1], pow2_of(cg))});
+                    const Pair u = swap_rows(Pair{odd_to_memory(vu[i], pow2_of(cu)), odd_to_memory(vu[i + 1], pow2_of(cu))});
+                    if (W.in0) {
+                        *reinterpret_cast<u32x4 *>(q + i * 32) = g.lo;
+                        *reinterpret_cast<u32x4 *>(q + wide + i * 32) = u.lo;
+                    }
+                    if (W.in1) {
+                        *reinterpret_cast<u32x4 *>(q + 32 * wide + i * 32) = g.hi;
+                        *reinterpret_cast<u32x4 *>(q + 33 * wide + i * 32) = u.hi;
                     }
                 }
-                if (R.in && l < 32) {
-                    uint8_t *s = B.q_scale + R.row * B.qs;
+                if (in && l < 32) {
+                    uint8_t *s = B.q_scale + row * B.qs;
                     s[b] = (uint8_t)cg;
                     s[B.ib + b] = (uint8_t)cu;
                     if (b == B.ib - 1) pad_scales(s, 2 * B.ib, B.qs);
@@ -592,7 +663,7 @@ struct GatedBackTile {
             }
             if (B.dots) {
                 const float sum = other_half_sum(R.dot);
-                if (R.in && l < 32) B.dots[R.row * B.ib + b] = sum;
+                if (in && l < 32) B.dots[row * B.ib + b] = sum;
             }
         });
     }
@@ -627,21 +698,30 @@ template <Keep kKeep>
 hipError_t forward(const ProductArgs &A, const typename GatedTile<kNone>::Args &B, hipStream_t s) {
     typedef GatedTile<kKeep> Tile;
     const typename Tile::Args C{B.up, B.weights, B.h, B.h_scale, B.kept, B.kept_scale, B.ib, B.hs, B.ks};
+    // 256 rows where tiles of 128 would take the 256 CUs more than one round, and groups
+    // mostly fill them.  Measured, us for 8 groups, hidden 4096, inter 2048 with tiles of
+    // 256, 128, 64 rows: 1000 rows a group 158, 175, 243; 400 rows 62, 74, 109; 200 rows
+    // 52, 41, 59; 100 rows 48, 34, 32.  5003 rows in 3 groups of 1999 x 1003 (160 tiles of
+    // 256): 32, 39, 46; 3001 rows in 5 of 1000 x 777 (84): 21, 15, 21.
     const int64_t rows = A.groups.M / A.groups.G;
-    auto enough = [&](int64_t tile) { return ceil_div(A.groups.M, tile) * ceil_div(A.N, kScaleBlock) >= 192; };
-    if (rows >= 256 && enough(256)) return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
-    if (rows >= 96) return launch_product<Tile, 128, 256, 64, 128, 4>(A, C, s);
-    return launch_product<Tile, 64, 256, 64, 64, 6>(A, C, s);
+    if (rows >= 256 && ceil_div(A.groups.M, 256) * ceil_div(A.N, kScaleBlock) > 128)
+        return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
+    if (rows >= 128) return launch_product<Tile, 128, 256, 32, 128, 4>(A, C, s);
+    return launch_product<Tile, 64, 256, 32, 128, 6>(A, C, s);
 }
 
 template <Keep kKeep>
 hipError_t backward(const ProductArgs &A, const typename GatedBackTile<kEight>::Args &B, hipStream_t s) {
     typedef GatedBackTile<kKeep> Tile;
     const typename Tile::Args C{B.weights, B.kept, B.kept_scale, B.dgu, B.q, B.q_scale, B.dots, B.ib, B.qs};
+    // The largest tiles where every CU has two, else two workgroups a CU.  Measured, us for
+    // 8 groups, hidden 4096, inter 2048 with tiles of 256 x 256, 128 x 128, 64 x 128: 8192
+    // rows a group 815, 952, 1218; 1000 rows (256 of the largest) 148, 130, 168; 400 rows 75, 59,
+    // 77; 200 rows 71, 37, 46; 100 rows 66, 34, 32.
     const int64_t rows = A.groups.M / A.groups.G;
-    auto enough = [&](int64_t tile) { return ceil_div(A.groups.M, tile) * ceil_div(A.N, tile) >= 192; };
-    if (rows >= 256 && enough(256)) return launch_product<Tile, 128, 256, 32, 128, 4>(A, C, s);
-    if (rows >= 96) return launch_product<Tile, 128, 128, 32, 128, 4>(A, C, s);
+    if (rows >= 256 && ceil_div(A.groups.M, 256) * ceil_div(A.N, 256) >= 512)
+        return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
+    if (rows >= 128) return launch_product<Tile, 128, 128, 32, 128, 4>(A, C, s);
     return launch_product<Tile, 64, 128, 32, 128, 6>(A, C, s);
 }
 
