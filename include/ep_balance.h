@@ -526,9 +526,13 @@ int ep_grouped_wgrad(const ep_grouped_wgrad_t *p, ep_stream_t stream);
  * fp32, every element written.  d(i) = dy_places[i] / rows_div, or i without dy_places;
  * r(i) likewise with x_places.  Given both, they are one and the same list.  A row whose
  * place is negative or too large adds nothing.
- *   dy       device bf16 [dy_rows][dy_stride]; dy_rows >= m without dy_places
+ *   dy       device bf16 [dy_rows][dy_stride], dy_stride < 2^31; dy_rows >= m without
+ *            dy_places
  *   x, x_scale  rows of k values in 8 bits, x_rows of them; x_rows >= m without x_places
  *   dy_places, x_places  device int32 [m] or NULL
+ *   ws       ep_wgrad_mixed_workspace_bytes(x_rows, k) bytes, 16-byte aligned: x in
+ *            bf16, which holds its values exactly; no state between calls, calls in
+ *            flight at once need their own
  */
 typedef struct ep_grouped_wgrad_mixed {
     const void *dy;
@@ -544,7 +548,10 @@ typedef struct ep_grouped_wgrad_mixed {
     const ep_layout_t *layout;
     float *out, *slot_out;
     int64_t out_stride, slot_out_stride;
+    void *ws;
+    size_t ws_bytes;
 } ep_grouped_wgrad_mixed_t;
+size_t ep_wgrad_mixed_workspace_bytes(int64_t x_rows, int64_t k);
 int ep_grouped_wgrad_mixed(const ep_grouped_wgrad_mixed_t *p, ep_stream_t stream);
 
 /*

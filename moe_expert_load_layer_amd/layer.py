@@ -63,7 +63,7 @@ class _CWgradMixed(ctypes.Structure):
     _fields_ = [("dy", _vp), ("dy_rows", _i64), ("dy_stride", _i64), ("x", _vp), ("x_scale", _vp), ("x_rows", _i64),
                 ("dy_places", _vp), ("x_places", _vp), ("rows_div", _i32), ("groups", _i32), ("offsets", _vp),
                 ("m", _i64), ("n", _i64), ("k", _i64), ("layout", ctypes.POINTER(_CLayout)), ("out", _vp),
-                ("slot_out", _vp), ("out_stride", _i64), ("slot_out_stride", _i64)]
+                ("slot_out", _vp), ("out_stride", _i64), ("slot_out_stride", _i64), ("ws", _vp), ("ws_bytes", _sz)]
 
 
 class _CExperts(ctypes.Structure):
@@ -90,6 +90,8 @@ def declare(L: ctypes.CDLL) -> None:
     L.ep_grouped_matmul.argtypes = [p(_CMatmul), _vp]
     L.ep_grouped_wgrad.argtypes = [p(_CWgrad), _vp]
     L.ep_grouped_wgrad_mixed.argtypes = [p(_CWgradMixed), _vp]
+    L.ep_wgrad_mixed_workspace_bytes.argtypes = [_i64, _i64]
+    L.ep_wgrad_mixed_workspace_bytes.restype = _sz
     L.ep_grouped_swiglu.argtypes = [p(_CSwiglu), _vp]
     L.ep_swiglu_backward_workspace_bytes.argtypes = [_i64, _i64]
     L.ep_swiglu_backward_workspace_bytes.restype = _sz
@@ -370,15 +372,29 @@ def _places(t: Optional[torch.Tensor], name: str) -> int:
     return t.shape[0]
 
 
+def _workspace(ws: Optional[torch.Tensor], need: int, device, stream):
+    """(address, bytes) of the workspace that is given, or of a new one."""
+    if ws is None:
+        ws = _held(torch.empty(max(16, need), dtype=torch.uint8, device=device), stream)
+    elif not (ws.is_cuda and ws.is_contiguous()):
+        raise EPBalanceError("ws must be a contiguous device tensor")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def ep_wgrad_mixed_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().ep_wgrad_mixed_workspace_bytes(int(rows), int(cols)))
+
+
 def ep_grouped_wgrad_mixed(dy: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
                            offsets: Optional[torch.Tensor] = None, cols: Optional[int] = None, dy_rows=None,
                            x_rows=None, rows_div: int = 1, layout: Optional[Layout] = None, out=None, slot_out=None,
-                           stream=None):
+                           ws=None, stream=None):
     """ep_grouped_wgrad with x in 8 bits: sum over the rows i of group g of dy[d(i)][n] x[r(i)][k] -> float32 [G][N][cols].
 
     x, x_scale as ep_quant_rows or ep_grouped_swiglu wrote rows of `cols` values (default: all that x has).
     d(i) = dy_rows[i] // rows_div, r(i) = x_rows[i] // rows_div (int32 [M]; None: i; both: the same list; negative or
-    too large: the row adds nothing).  With a layout: (native, spare), as ep_grouped_wgrad."""
+    too large: the row adds nothing).  With a layout: (native, spare), as ep_grouped_wgrad.
+    ws: ep_wgrad_mixed_workspace_bytes(rows of x, cols) bytes."""
     ds = _rows(dy, (torch.bfloat16,), "dy")
     if x.dim() != 2 or x.shape[1] % 128:
         raise EPBalanceError(f"x must be [rows][columns up to a multiple of 128], got shape {tuple(x.shape)}")
@@ -404,6 +420,7 @@ def ep_grouped_wgrad_mixed(dy: torch.Tensor, x: torch.Tensor, x_scale: torch.Ten
                      None if dy_rows is None else dy_rows.data_ptr(), None if x_rows is None else x_rows.data_ptr(),
                      rows_div, G, None if offsets is None else offsets.data_ptr(), M, N, K, None, out.data_ptr(), None,
                      out.stride(0), 0)
+    p.ws, p.ws_bytes = _workspace(ws, ep_wgrad_mixed_workspace_bytes(x.shape[0], K), dy.device, stream)
     if layout is not None:
         p.layout = ctypes.pointer(layout.c)
         slot_out = _gradient(slot_out, (layout.num_spare, N, K), dy.device, "slot_out", stream)
@@ -529,14 +546,9 @@ def ep_grouped_swiglu_backward(dy: torch.Tensor, dy_scale: torch.Tensor, down: t
         p.weights_count = _pair_weights(weights, None if rows is not None else M)
         pairs = M if pos is None else _places(pos, "pos")
         grad_weights = _out(grad_weights, weights_dtype, (pairs,), dy.device, "grad_weights", stream)
-        need = ep_swiglu_backward_workspace_bytes(M, I)
-        if ws is None:
-            ws = _held(torch.empty(max(16, need), dtype=torch.uint8, device=dy.device), stream)
-        elif not (ws.is_cuda and ws.is_contiguous()):
-            raise EPBalanceError("ws must be a contiguous device tensor")
         p.weights, p.grad_weights, p.grad_weights_dtype = weights.data_ptr(), grad_weights.data_ptr(), _FLOATS[weights_dtype]
         p.pos, p.pairs = None if pos is None else pos.data_ptr(), pairs
-        p.ws, p.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        p.ws, p.ws_bytes = _workspace(ws, ep_swiglu_backward_workspace_bytes(M, I), dy.device, stream)
     elif pos is not None or grad_weights is not None:
         raise EPBalanceError("grad_weights and pos need weights")
     if layout is not None:
