@@ -490,8 +490,8 @@ def run_path(topk_ids: torch.Tensor, layout: Layout, stream=None):
 
 
 from .layer import (  # noqa: E402,F401  (the operators around the balancer)
-    EP_DTYPE_BF16, EP_DTYPE_F32, EP_DTYPE_FP8, EP_MAX_FEW_TOKENS, AdamW, ExpertRows, ep_few_tokens_workspace_bytes,
-    ep_gate_topk, ep_gate_topk_backward, ep_grouped_matmul, ep_grouped_swiglu, ep_grouped_swiglu_backward,
-    ep_grouped_wgrad, ep_grouped_wgrad_mixed, ep_moe_combine, ep_moe_few_tokens, ep_quant_blocks, ep_quant_rows,
-    ep_scale_stride, ep_swiglu_backward_workspace_bytes, ep_swiglu_quant,
-    ep_wgrad_mixed_workspace_bytes, run_layer)
+    EP_DTYPE_BF16, EP_DTYPE_F32, EP_DTYPE_FP8, EP_MAX_FEW_TOKENS, AdamW, ExpertBackwardRows, ExpertRows,
+    ep_few_tokens_workspace_bytes, ep_gate_topk, ep_gate_topk_backward, ep_grouped_matmul, ep_grouped_swiglu,
+    ep_grouped_swiglu_backward, ep_grouped_wgrad, ep_grouped_wgrad_mixed, ep_moe_combine, ep_moe_few_tokens,
+    ep_quant_blocks, ep_quant_rows, ep_scale_stride, ep_swiglu_backward_workspace_bytes, ep_swiglu_quant,
+    ep_wgrad_mixed_workspace_bytes, run_layer, run_layer_backward, run_layer_train)

@@ -12,7 +12,7 @@ import numpy as np
 import torch
 
 from . import (EPBalanceError, Layout, _check, _CLayout, _held, ep_dispatch_layout, ep_load_histogram, ep_plan_quota,
-               ep_slot_fill, lib)
+               ep_replica_grad_reduce, ep_slot_fill, lib)
 from . import _arg as _arg_or_raise
 
 EP_DTYPE_F32, EP_DTYPE_BF16, EP_DTYPE_FP8 = 0, 1, 2
@@ -620,27 +620,78 @@ class ExpertRows:
     """8-bit weights of a layer's experts, one packed row of bytes each: gate above up [2 I][H], down [H][I], then
     their scales.  A row is what ep_slot_fill copies, so a buffer of spare slots has the same views.
 
-    ep_moe_few_tokens takes gate and up apart: gate_up and gate_up_scale split into halves where inter is a multiple
-    of 128.  Elsewhere one scale byte covers rows of both, and the halves need an ep_quant_blocks of their own."""
+    gate, up, gate_scale, up_scale are the halves of gate_up, which ep_grouped_swiglu and ep_moe_few_tokens take.  One
+    scale byte may cover rows of both where inter is no multiple of 128: then they are None, unless the rows are made
+    with apart=True, which gives either its own scales and leaves gate_up None."""
 
-    def __init__(self, count: int, hidden: int, inter: int, device):
+    def __init__(self, count: int, hidden: int, inter: int, device, apart: bool = False):
         self.hidden, self.inter = hidden, inter
         hp, ip, hb, ib = _up128(hidden), _up128(inter), _up128(hidden) // 128, _up128(inter) // 128
-        nb = _up128(2 * inter) // 128
+        self._halves = apart or inter % 128 == 0
+        nb = 2 * ib if self._halves else _up128(2 * inter) // 128
         ends = np.cumsum([2 * inter * hp, hidden * ip, nb * hb, hb * ib])
         self.rows = torch.zeros((count, int(-(-ends[3] // 16) * 16)), dtype=torch.uint8, device=device)
         part = lambda a, b, n, k: self.rows[:, a:b].unflatten(1, (n, k))     # noqa: E731
         self.gate_up = part(0, ends[0], 2 * inter, hp).view(_FP8)
         self.down = part(ends[0], ends[1], hidden, ip).view(_FP8)
         self.gate_up_scale, self.down_scale = part(ends[1], ends[2], nb, hb), part(ends[2], ends[3], hb, ib)
+        self.gate = self.up = self.gate_scale = self.up_scale = None
+        if self._halves:
+            self.gate, self.up = self.gate_up[:, :inter], self.gate_up[:, inter:]
+            self.gate_scale, self.up_scale = self.gate_up_scale[:, :ib], self.gate_up_scale[:, ib:]
+        if inter % 128 and apart:
+            self.gate_up = self.gate_up_scale = None
 
     def load(self, gate_up: torch.Tensor, down: torch.Tensor) -> "ExpertRows":
         """Rounds fp32 or bf16 matrices [E][2 I][H] and [E][H][I] into the rows."""
-        for w, q, s in ((gate_up, self.gate_up, self.gate_up_scale), (down, self.down, self.down_scale)):
+        if self.gate_up is None:
+            parts = [(gate_up[:, :self.inter], self.gate, self.gate_scale),
+                     (gate_up[:, self.inter:], self.up, self.up_scale)]
+        else:
+            parts = [(gate_up, self.gate_up, self.gate_up_scale)]
+        for w, q, s in parts + [(down, self.down, self.down_scale)]:
             wq, ws = ep_quant_blocks(w)
             q.view(torch.uint8).copy_(wq.view(torch.uint8))
             s.copy_(ws)
         return self
+
+
+class ExpertBackwardRows:
+    """The same experts' matrices transposed, as a backward pass takes them: down_t [I][H up to 128], both_t [H][2 * (I up
+    to 128)] (gate's transpose beside up's, each up to whole blocks) and their scales, packed rows as ExpertRows'."""
+
+    def __init__(self, count: int, hidden: int, inter: int, device):
+        self.hidden, self.inter = hidden, inter
+        hp, ip, hb, ib = _up128(hidden), _up128(inter), _up128(hidden) // 128, _up128(inter) // 128
+        ends = np.cumsum([hidden * 2 * ip, inter * hp, hb * 2 * ib, ib * hb])
+        self.rows = torch.zeros((count, int(-(-ends[3] // 16) * 16)), dtype=torch.uint8, device=device)
+        part = lambda a, b, n, k: self.rows[:, a:b].unflatten(1, (n, k))     # noqa: E731
+        self.both_t = part(0, ends[0], hidden, 2 * ip).view(_FP8)
+        self.down_t = part(ends[0], ends[1], inter, hp).view(_FP8)
+        self.both_t_scale, self.down_t_scale = part(ends[1], ends[2], hb, 2 * ib), part(ends[2], ends[3], ib, hb)
+
+    def load(self, gate_up: torch.Tensor, down: torch.Tensor) -> "ExpertBackwardRows":
+        """Rounds the matrices that ExpertRows.load takes."""
+        I, ip, ib = self.inter, _up128(self.inter), _up128(self.inter) // 128
+        for w, q, s in ((gate_up[:, :I], self.both_t[:, :, :ip], self.both_t_scale[:, :, :ib]),
+                        (gate_up[:, I:], self.both_t[:, :, ip:], self.both_t_scale[:, :, ib:]),
+                        (down, self.down_t, self.down_t_scale)):
+            wq, ws = ep_quant_blocks(w, transpose=True)
+            q.view(torch.uint8).copy_(wq.view(torch.uint8))
+            s.copy_(ws)
+        return self
+
+
+def _route(logits, k, layout, experts, slots, bias, num_groups, topk_groups, scale):
+    """The balanced path of one layer: gate, load, plan, dispatch order, replicas into the spare slots."""
+    ids, weights = ep_gate_topk(logits, k, bias, num_groups, topk_groups, scale)
+    pairs = ids.view(1, -1)
+    load, ws, status = ep_load_histogram(pairs, layout)
+    plan = ep_plan_quota(load, layout, status=status)
+    offsets, pos, src = ep_dispatch_layout(pairs, layout, plan.phy_quota, plan.log2phy, plan.logcnt, ws)
+    if layout.num_spare:
+        ep_slot_fill(experts.rows, plan.phy2log[0], layout, slots.rows)
+    return ids, weights, plan, status, offsets, pos, src
 
 
 def run_layer(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layout, experts: ExpertRows, slots: ExpertRows,
@@ -654,13 +705,10 @@ def run_layer(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layout, exp
     if x.dim() != 2 or logits.dim() != 2 or x.shape[0] != logits.shape[0]:
         raise EPBalanceError(f"x [tokens][hidden] and logits [tokens][experts] must have the same tokens, got "
                              f"{tuple(x.shape)} and {tuple(logits.shape)}")
-    ids, weights = ep_gate_topk(logits, k, bias, num_groups, topk_groups, scale)
-    pairs = ids.view(1, -1)
-    load, ws, status = ep_load_histogram(pairs, layout)
-    plan = ep_plan_quota(load, layout, status=status)
-    offsets, pos, src = ep_dispatch_layout(pairs, layout, plan.phy_quota, plan.log2phy, plan.logcnt, ws)
-    if layout.num_spare:
-        ep_slot_fill(experts.rows, plan.phy2log[0], layout, slots.rows)
+    if experts.gate_up is None:
+        raise EPBalanceError("experts made apart with inter no multiple of 128 have no gate_up")
+    ids, weights, plan, status, offsets, pos, src = _route(logits, k, layout, experts, slots, bias, num_groups,
+                                                           topk_groups, scale)
     spare = (slots.gate_up, slots.gate_up_scale, slots.down, slots.down_scale) if layout.num_spare else (None,) * 4
     xq, xs = ep_quant_rows(x)
     up = ep_grouped_matmul(xq, xs, experts.gate_up, experts.gate_up_scale, offsets[0], rows=src[0], rows_div=k,
@@ -671,6 +719,78 @@ def run_layer(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layout, exp
     out = ep_moe_combine(y, pos.view(-1, k), weights)
     return dict(out=out, ids=ids, weights=weights, plan=plan, status=status, offsets=offsets[0], pos=pos[0],
                 src=src[0], up=up, h=h, y=y)
+
+
+def run_layer_train(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layout, experts: ExpertRows,
+                    slots: ExpertRows, bias=None, num_groups: int = 1, topk_groups: int = 1, scale: float = 1.0,
+                    keep: torch.dtype = _FP8):
+    """run_layer's layer in a training step: returns a dict with out bf16 [tokens][H], ids, weights, plan, status,
+    offsets, pos, src, and what run_layer_backward needs besides.
+
+    What is kept of the activations for it: x and the weighted silu(g) u in 8 bits, as the products take them, and g
+    and u in `keep` (torch.float8_e4m3fn or torch.bfloat16).  experts and slots need gate and up with their own scales
+    (ExpertRows)."""
+    if x.dim() != 2 or logits.dim() != 2 or x.shape[0] != logits.shape[0]:
+        raise EPBalanceError(f"x [tokens][hidden] and logits [tokens][experts] must have the same tokens, got "
+                             f"{tuple(x.shape)} and {tuple(logits.shape)}")
+    if experts.gate is None or (layout.num_spare and slots.gate is None):
+        raise EPBalanceError("experts and slots need gate and up with their own scales: inter a multiple of 128, or "
+                             "ExpertRows(apart=True)")
+    if keep not in (_FP8, torch.bfloat16):
+        raise EPBalanceError(f"keep must be torch.float8_e4m3fn or torch.bfloat16, got {keep}")
+    ids, weights, plan, status, offsets, pos, src = _route(logits, k, layout, experts, slots, bias, num_groups,
+                                                           topk_groups, scale)
+    spare = layout.num_spare > 0
+    xq, xs = ep_quant_rows(x)
+    h, hs, kept, ks = ep_grouped_swiglu(
+        xq, xs, experts.gate, experts.gate_scale, experts.up, experts.up_scale, offsets[0], rows=src[0], rows_div=k,
+        weights=weights.view(-1), keep=keep, layout=layout, slot_gate=slots.gate if spare else None,
+        slot_gate_scale=slots.gate_scale if spare else None, slot_up=slots.up if spare else None,
+        slot_up_scale=slots.up_scale if spare else None)
+    y = ep_grouped_matmul(h, hs, experts.down, experts.down_scale, offsets[0], layout=layout,
+                          slot_w=slots.down if spare else None, slot_w_scale=slots.down_scale if spare else None)
+    out = ep_moe_combine(y, pos.view(-1, k), torch.ones_like(weights))
+    return dict(out=out, ids=ids, weights=weights, plan=plan, status=status, offsets=offsets[0], pos=pos[0], src=src[0],
+                x=(xq, xs), h=(h, hs), kept=(kept, ks), top_k=k, scale=scale, logits_dtype=logits.dtype,
+                hidden=x.shape[1], inter=experts.inter)
+
+
+def run_layer_backward(kept: dict, grad_out: torch.Tensor, layout: Layout, experts: ExpertBackwardRows,
+                       slots: ExpertBackwardRows):
+    """The gradients of run_layer_train's layer, from what it returned and grad_out, bf16 [tokens][H].
+
+    Returns a dict: x bf16 [tokens][H], logits [tokens][E] in the logits' type, gate_up float32 [E][2 I][H], down
+    float32 [E][H][I], the replicas' shares folded into their experts'.  Roundings to 8 bits count as the identity.
+    experts: the native experts' transposed matrices, slots: the spare slots' (filled here)."""
+    k, H, I = kept["top_k"], kept["hidden"], kept["inter"]
+    ids, weights, plan, offsets, pos, src = (kept[n] for n in ("ids", "weights", "plan", "offsets", "pos", "src"))
+    _arg(grad_out, torch.bfloat16, (ids.shape[0], H), "grad_out")
+    if (experts.hidden, experts.inter) != (H, I):
+        raise EPBalanceError(f"experts must be of hidden {H} and inter {I}, got {experts.hidden} and {experts.inter}")
+    spare = layout.num_spare > 0
+    if spare and H * I % 4:
+        raise EPBalanceError(f"with spare slots hidden * inter must be a multiple of 4, got {H} * {I}")
+    if spare:
+        ep_slot_fill(experts.rows, plan.phy2log[0], layout, slots.rows)
+    dq, ds = ep_quant_rows(grad_out)
+    grad, q, qs, dw = ep_grouped_swiglu_backward(
+        dq, ds, experts.down_t, experts.down_t_scale, *kept["kept"], offsets, rows=src, rows_div=k,
+        weights=weights.view(-1), pos=pos, layout=layout, slot_down=slots.down_t if spare else None,
+        slot_down_scale=slots.down_t_scale if spare else None)
+    dx = ep_grouped_matmul(q, qs, experts.both_t, experts.both_t_scale, offsets, layout=layout,
+                           slot_w=slots.both_t if spare else None,
+                           slot_w_scale=slots.both_t_scale if spare else None)
+    out = dict(x=ep_moe_combine(dx, pos.view(-1, k), torch.ones_like(weights)),
+               logits=ep_gate_topk_backward(ids, weights, dw.view(-1, k), layout.num_experts, kept["scale"],
+                                            kept["logits_dtype"]))
+    for name, dy, dy_rows, (xq, xs), x_rows, cols in (("gate_up", grad, None, kept["x"], src, H),
+                                                      ("down", grad_out, src, kept["h"], None, I)):
+        native, replicas = ep_grouped_wgrad_mixed(dy, xq, xs, offsets, cols=cols, dy_rows=dy_rows, x_rows=x_rows,
+                                                  rows_div=k, layout=layout)
+        if spare:
+            ep_replica_grad_reduce(native.flatten(1), replicas.flatten(1), plan.log2phy[0], plan.logcnt[0], layout)
+        out[name] = native
+    return out
 
 
 class AdamW:

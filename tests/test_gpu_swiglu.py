@@ -24,7 +24,8 @@ def dev():
 def _rows(rng, M, K, dev, std=1.0):
     a = rng.normal(0, std, (M, K)) * np.exp(0.5 * rng.normal(0, 1, (M, 1)))
     a[:, rng.random(K) < 0.02] *= 20
-    return torch.from_numpy(a.astype(np.float32)).to(BF16).to(dev)
+    out = torch.empty((M, K), dtype=BF16, device=dev)
+    return out.copy_(torch.from_numpy(a.astype(np.float32)).to(dev))
 
 
 class Case:
