@@ -92,14 +92,29 @@ __device__ __forceinline__ constexpr int frag_row(int wn, int i) {
     return i / (FN / 2) * (BN / 2) + wn * (WN / 2) + i % (FN / 2) * 32;
 }
 
+// The same bytes under their scale as bf16, which holds e4m3 times a power of two
+// exactly.  A lane's 32 are consecutive in K; the 16-bit instruction sums over 8 of
+// them (and over the 8 of the lane in the other half) at a time, in both operands alike.
+__device__ __forceinline__ void open_frag(const i32x8 &f, int code, bf16x8 (&v)[4]) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const float scale = __builtin_bit_cast(float, (uint32_t)code << 23);
+#pragma unroll
+    for (int q = 0; q < 8; q++) {
+        const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[q], scale, false);
+        const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[q], scale, true);
+        v[q / 2][q % 2 * 4] = lo[0], v[q / 2][q % 2 * 4 + 1] = lo[1];
+        v[q / 2][q % 2 * 4 + 2] = hi[0], v[q / 2][q % 2 * 4 + 3] = hi[1];
+    }
+}
+
 // One K step of a wave: multiplies the operands fx, fw with the scales sx, sw
 // while the next step's are read from `next` (nx, ns; fw right after the
 // products that use it) and a later step's loads go into `fill`.  The empty asm
 // statements hold the products in this order: together at the front, they would
 // leave nothing to wait behind.
-template <int kMatrices, int BM, int BN, int WN, int FM, int FN, int kLoads, int kWaves>
+template <bool kExact, int kMatrices, int BM, int BN, int WN, int FM, int FN, int kLoads, int kWaves>
 __device__ __forceinline__ void product_step(const uint8_t *next, uint32_t fill, const uint8_t *(&src)[kLoads],
-                                             int ahead, int xrow, int wn, int lane, const uint8_t *xs,
+                                             int ahead, int xrow, int wn, int lane, bool tall, const uint8_t *xs,
                                              const uint8_t *ws, int block, const i32x8 (&fx)[FM], i32x8 (&nx)[FM], i32x8 (&fw)[FN],
                                              const int (&sx)[FM], int (&ns)[FM], int (&sw)[kMatrices],
                                              f32x16 (&acc)[FN][FM]) {
@@ -107,12 +122,27 @@ __device__ __forceinline__ void product_step(const uint8_t *next, uint32_t fill,
     int nsw[kMatrices];
 #pragma unroll
     for (int i = 0; i < kMatrices; i++) nsw[i] = ws[block * 4 + i * kScaleBlocks * 4];
+    bf16x8 ox[FM][4];
+    if constexpr (kExact)
+#pragma unroll
+        for (int j = 0; j < FM; j++)
+            if (j == 0 || tall) open_frag(fx[j], sx[j], ox[j]);
 #pragma unroll
     for (int i = 0; i < FN; i++) {
         asm volatile("" : "+v"(fw[i]));
+        if constexpr (kExact) {
+            bf16x8 ow[4];
+            open_frag(fw[i], sw[i * kMatrices / FN], ow);
+#pragma unroll
+            for (int j = 0; j < FM; j++)
+                if (j == 0 || tall)
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ow[q], ox[j][q], acc[i][j], 0, 0, 0);
+        }
 #pragma unroll
         for (int j = 0; j < FM; j++)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[i], fx[j], acc[i][j], 0, 0, 0,
+            if constexpr (!kExact) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[i], fx[j], acc[i][j], 0, 0, 0,
                                                                         sw[i * kMatrices / FN], 0, sx[j]);
         if (i == 0) {
 #pragma unroll
@@ -163,7 +193,11 @@ constexpr int waves_a_simd(int BM, int BN, int WM, int WN, int kStages) {
 //               repeats or is, and the row of x (-1: none)
 //   store(...)  a tile's sums, by all waves at once
 //   tail(...)   the rows past the last group, by all threads
-template <class Store, int BM, int BN, int WM, int WN, int kStages, bool kChained>
+//
+// kExact: each operand opened to bf16 and multiplied by the 16-bit instruction, whose
+// sums are fp32's, at half the rate and with 16 conversions a fragment; for products
+// that wait for their weights anyway, where the sums are rounded to 8 bits again.
+template <class Store, int BM, int BN, int WM, int WN, int kStages, bool kChained, bool kExact>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN, WM, WN, kStages)) void product_kernel(const ProductArgs A,
                                                                                    const typename Store::Args B) {
     constexpr int kMatrices = Store::kMatrices;
@@ -332,6 +366,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
             const bool more = at + walk.stride < walk.to;
             // a long store needs the registers that the loop's addresses would keep
             const int lane = Store::kLong ? lane_now() : lane_id();
+            // exact sums leave out rows of 32 that the tile does not have
+            const bool tall = kExact && __builtin_amdgcn_readfirstlane(tiles[buf].m0 + wm * WM + 32 < tiles[buf].m1);
             const int chunks = (A.kb + kScaleBlocks - 1) / kScaleBlocks;
             int ahead = kStep;
             // A step: its operands are in x, c and fw, the next one's (block `block` of
@@ -344,9 +380,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
                 __syncthreads();
                 const int after = slot == kStages - 1 ? 0 : slot + 1;
                 const uint8_t *xs = scales + chunk;
-                product_step<kMatrices, BM, BN, WN, FM, FN, kLoads, kWaves>(
-                    stages + after * kStage, ring + slot * kStage, src, ahead, wm * WM, wn, lane, xs, xs + wscale,
-                    block, x, nx, fw, c, nc, sw, acc);
+                product_step<kExact, kMatrices, BM, BN, WN, FM, FN, kLoads, kWaves>(
+                    stages + after * kStage, ring + slot * kStage, src, ahead, wm * WM, wn, lane, tall, xs,
+                    xs + wscale, block, x, nx, fw, c, nc, sw, acc);
                 slot = after;
             };
             // Between the steps at which something happens besides, the loop is bare.
@@ -403,14 +439,15 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
         Store::tail(A, B, (int64_t)blockIdx.x * kThreads + threadIdx.x, (int64_t)gridDim.x * kThreads);
 }
 
-template <class Store, int BM, int BN, int WM, int WN, int kStages>
+template <class Store, int BM, int BN, int WM, int WN, int kStages, bool kExact = false>
 hipError_t launch_product(const ProductArgs &A, const typename Store::Args &B, hipStream_t s) {
     constexpr int kThreads = (BM / WM) * (BN / WN) * kWave;
     int64_t blocks = tile_blocks(A.groups.M, A.groups.G, A.N, BM, BN / Store::kMatrices);
     // As many workgroups as the card holds; where a tile's steps are too few to be
     // chained, as many as there are tiles.
-    const auto kernel = tiles_chained(A.kb * kParts, kStages) ? product_kernel<Store, BM, BN, WM, WN, kStages, true>
-                                                              : product_kernel<Store, BM, BN, WM, WN, kStages, false>;
+    const auto kernel = tiles_chained(A.kb * kParts, kStages)
+                            ? product_kernel<Store, BM, BN, WM, WN, kStages, true, kExact>
+                            : product_kernel<Store, BM, BN, WM, WN, kStages, false, kExact>;
     if (tiles_chained(A.kb * kParts, kStages)) {
         const int64_t resident = resident_blocks((const void *)kernel, kThreads, 0) / 8 * 8;
         if (resident > 0 && resident < blocks) blocks = resident;

@@ -194,13 +194,21 @@ def test_backward(dev, shape, keep):
     assert torch.equal(half, dw.to(BF16))
 
 
-def test_fused_and_apart_agree(dev):
-    """The block in one product against the grouped product in bf16 and the step on its own: 2^-9 apart before the 8 bits."""
-    c = Case(dev, [300, 211], 640, 256, 4, weights=False)
+@pytest.mark.parametrize("sizes,inter", [([300, 211], 256), ([3000, 2111], 256), ([3000, 2111], 384)], ids=str)
+def test_fused_and_apart_agree(dev, sizes, inter):
+    """The block in one product against the grouped product in bf16 and the step on its own: 2^-9 apart before the 8
+    bits.  With many rows of many columns they have the same sums, rounded once; else exact sums against those: their
+    bound and a rounding of each, 2^-8 of a value."""
+    c = Case(dev, sizes, 640, inter, 4, weights=False)
     both = torch.cat([c.gate[0].view(torch.uint8), c.up[0].view(torch.uint8)], 1).view(FP8)
     apart = ep.ep_grouped_matmul(*c.xq, both, torch.cat([c.gate[1], c.up[1]], 1), c.offsets, rows=c.rows, rows_div=4)
     h, hs, kept, _ = c.run_forward(BF16)
-    assert torch.equal(kept, apart)                   # the same sums, rounded once
+    if inter > 256:
+        assert torch.equal(kept, apart)
+    else:
+        r = c.forward()
+        v, e = torch.cat([r["g"], r["u"]], 1).abs(), torch.cat([r["eg"], r["eu"]], 1)
+        assert ((kept.double() - apart.double()).abs() <= e + 2 * 2.0 ** -8 * (v + e)).all()
     q, s = ep.ep_swiglu_quant(apart)
     one, two = S.values(h, hs), S.values(q, s)
     assert float((one - two).norm()) < 0.05 * float(two.norm())

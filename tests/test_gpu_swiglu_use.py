@@ -195,18 +195,27 @@ def test_past_31_bits(dev, keep):
     assert kept.numel() > 2 ** 31 and grad.numel() > 2 ** 31
     few = slice(M - 40, M)
     t = rows[few].long()
-    small = ep.ep_grouped_swiglu(xq[0][t], xq[1][t], gate[0][1:], gate[1][1:], up[0][1:], up[1][1:], weights=weights[t],
-                                 keep=keep)
-    for a, b in zip((h, hs, kept), small):
-        assert torch.equal(a[few].view(torch.uint8), b.view(torch.uint8))
-    gs, q2, qs2, dw2 = ep.ep_grouped_swiglu_backward(dq[0][t], dq[1][t], down[0][1:], down[1][1:], small[2], small[3],
-                                                     weights=weights[t])
-    assert torch.equal(grad[few], gs) and torch.equal(q[few].view(torch.uint8), q2.view(torch.uint8))
-    assert torch.equal(dw[:40].flip(0), dw2) and torch.equal(qs[few], qs2)
+    xv, dv, w = S.values(*xq), S.values(*dq), weights[t].double()[:, None]
+    g, eg, u, eu, hw, eh = S.forward(xv[t], S.matrix(gate[0][1], gate[1][1], hidden), S.matrix(up[0][1], up[1][1], hidden), w)
+    S.check_fp8(h[few], hs[few], hw, eh, "h")
+    if keep is FP8:
+        full = S.values(kept[few], ks[few])
+        for name, at, want, e in (("g", 0, g, eg), ("u", 1, u, eu)):
+            S.check_fp8(kept[few, at * inter:(at + 1) * inter], ks[few, at * 16:(at + 1) * 16], want, e, name)
+    else:
+        full = kept[few].double()
+        S.check_bf16(kept[few], torch.cat([g, u], 1), torch.cat([eg, eu], 1), "kept")
+    back = S.matrix(down[0][1], down[1][1], hidden)
+    d, ed = dv[t] @ back.t(), S.DROPPED * (dv[t].abs() @ back.abs().t())
+    dg, edg, du, edu, terms, et = S.backward(d, ed, full[:, :inter], full[:, inter:], w)
+    S.check_bf16(grad[few], torch.cat([dg, du], 1), torch.cat([edg, edu], 1), "gradients")
+    for at, want, e in ((0, dg, edg), (1, du, edu)):
+        S.check_fp8(q[few, at * inter:(at + 1) * inter], qs[few, at * 16:(at + 1) * 16], want, e, "in 8 bits")
+    bound = et.sum(1) + (128 + 16) * 2.0 ** -24 * terms.abs().sum(1)
+    assert ((dw[:40].flip(0).double() - terms.sum(1)).abs() <= bound).all()
     if keep is FP8:
         return
     got = ep.ep_grouped_wgrad_mixed(grad, *xq, off, cols=hidden, x_rows=rows)[1]
-    xv = S.values(*xq)
     want, size = torch.zeros(2 * inter, hidden, dtype=torch.float64, device=dev), torch.zeros_like(got, dtype=torch.float64)
     for at in range(1000, M, 100_000):
         i = slice(at, min(M, at + 100_000))
