@@ -114,7 +114,7 @@ __device__ __forceinline__ void open_frag(const i32x8 &f, int code, bf16x8 (&v)[
 // leave nothing to wait behind.
 template <bool kExact, int kMatrices, int BM, int BN, int WN, int FM, int FN, int kLoads, int kWaves>
 __device__ __forceinline__ void product_step(const uint8_t *next, uint32_t fill, const uint8_t *(&src)[kLoads],
-                                             int ahead, int xrow, int wn, int lane, bool tall, const uint8_t *xs,
+                                             int ahead, int xrow, int wn, int lane, const uint8_t *xs,
                                              const uint8_t *ws, int block, const i32x8 (&fx)[FM], i32x8 (&nx)[FM], i32x8 (&fw)[FN],
                                              const int (&sx)[FM], int (&ns)[FM], int (&sw)[kMatrices],
                                              f32x16 (&acc)[FN][FM]) {
@@ -125,8 +125,7 @@ __device__ __forceinline__ void product_step(const uint8_t *next, uint32_t fill,
     bf16x8 ox[FM][4];
     if constexpr (kExact)
 #pragma unroll
-        for (int j = 0; j < FM; j++)
-            if (j == 0 || tall) open_frag(fx[j], sx[j], ox[j]);
+        for (int j = 0; j < FM; j++) open_frag(fx[j], sx[j], ox[j]);
 #pragma unroll
     for (int i = 0; i < FN; i++) {
         asm volatile("" : "+v"(fw[i]));
@@ -134,11 +133,10 @@ __device__ __forceinline__ void product_step(const uint8_t *next, uint32_t fill,
             bf16x8 ow[4];
             open_frag(fw[i], sw[i * kMatrices / FN], ow);
 #pragma unroll
-            for (int j = 0; j < FM; j++)
-                if (j == 0 || tall)
+            for (int q = 0; q < 4; q++)
 #pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ow[q], ox[j][q], acc[i][j], 0, 0, 0);
+                for (int j = 0; j < FM; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ow[q], ox[j][q], acc[i][j], 0, 0, 0);
         }
 #pragma unroll
         for (int j = 0; j < FM; j++)
@@ -366,8 +364,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
             const bool more = at + walk.stride < walk.to;
             // a long store needs the registers that the loop's addresses would keep
             const int lane = Store::kLong ? lane_now() : lane_id();
-            // exact sums leave out rows of 32 that the tile does not have
-            const bool tall = kExact && __builtin_amdgcn_readfirstlane(tiles[buf].m0 + wm * WM + 32 < tiles[buf].m1);
             const int chunks = (A.kb + kScaleBlocks - 1) / kScaleBlocks;
             int ahead = kStep;
             // A step: its operands are in x, c and fw, the next one's (block `block` of
@@ -381,8 +377,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN,
                 const int after = slot == kStages - 1 ? 0 : slot + 1;
                 const uint8_t *xs = scales + chunk;
                 product_step<kExact, kMatrices, BM, BN, WN, FM, FN, kLoads, kWaves>(
-                    stages + after * kStage, ring + slot * kStage, src, ahead, wm * WM, wn, lane, tall, xs,
-                    xs + wscale, block, x, nx, fw, c, nc, sw, acc);
+                    stages + after * kStage, ring + slot * kStage, src, ahead, wm * WM, wn, lane, xs, xs + wscale,
+                    block, x, nx, fw, c, nc, sw, acc);
                 slot = after;
             };
             // Between the steps at which something happens besides, the loop is bare.

@@ -698,14 +698,18 @@ __global__ __launch_bounds__(kDotThreads) void pair_dots_kernel(const float *__r
 // row has few, or a sum has few terms that could make up for one another: a sum of
 // 8-bit products that is off by 2^-14 sends one in 300 of the values rounded to 8 bits
 // the other way, by a sixteenth of itself, which thousands of others outweigh and a few
-// large ones do not.  These take the exact sums.  Over 1500 random shapes with rows and
-// columns of different sizes the error to 64 bits then stays below 5e-3 in all but a
-// few (2.6e-3 as a rule; 1.7e-3 is the bf16 outputs' own), without them in 5 % it does
-// not.  Cost, us forward and backward: 65536 rows, 2048 x 200 180 + 110 against 107 + 86; 30340
-// rows, 754 x 143 41 + 40 against 27 + 35; 8 rows of 8 groups, 4096 x 2048 35 against 26 forward.
-bool few(const ProductArgs &A) {
-    return A.N <= 256 || A.kb <= 2 || (int64_t)A.groups.M * A.N < (1 << 19);
+// large ones do not.  These take the exact sums.  Over 1000 random shapes, some rows and
+// columns of them much larger than others, the error to 64 bits passed 5e-3 in 5 % of
+// the shapes without them (1.7e-3 is the bf16 outputs' own, 2.6e-3 the rule).  The forward
+// kernel's values go on into everything, so it takes them up to 4 times as many.
+//
+// Cost, us forward and backward: 65536 rows, 2048 x 200 180 + 110 against 107 + 86; 30340 rows,
+// 754 x 143 41 + 40 against 27 + 35; 8 rows of 8 groups, 4096 x 2048 34 against 28 forward;
+// 640 rows of 8 groups, 4096 x 1024 36 against 30.
+bool few(const ProductArgs &A, int64_t values) {
+    return A.N <= 256 || A.kb <= 2 || (int64_t)A.groups.M * A.N < values;
 }
+constexpr int64_t kFewForward = 1 << 21, kFewBackward = 1 << 19;
 
 template <Keep kKeep>
 hipError_t forward(const ProductArgs &A, const typename GatedTile<kNone>::Args &B, hipStream_t s) {
@@ -717,10 +721,11 @@ hipError_t forward(const ProductArgs &A, const typename GatedTile<kNone>::Args &
     // 52, 41, 59; 100 rows 48, 34, 32.  5003 rows in 3 groups of 1999 x 1003 (160 tiles of
     // 256): 32, 39, 46; 3001 rows in 5 of 1000 x 777 (84): 21, 15, 21.
     const int64_t rows = A.groups.M / A.groups.G;
-    if (rows >= 256 && !few(A) && ceil_div(A.groups.M, 256) * ceil_div(A.N, kScaleBlock) > 128)
+    if (few(A, kFewForward))
+        return rows >= 128 ? launch_product<Tile, 128, 256, 32, 128, 4, true>(A, C, s)
+                           : launch_product<Tile, 64, 256, 32, 128, 6, true>(A, C, s);
+    if (rows >= 256 && ceil_div(A.groups.M, 256) * ceil_div(A.N, kScaleBlock) > 128)
         return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
-    if (few(A) && rows >= 128) return launch_product<Tile, 128, 256, 32, 128, 4, true>(A, C, s);
-    if (few(A)) return launch_product<Tile, 64, 256, 64, 64, 6, true>(A, C, s);
     if (rows >= 128) return launch_product<Tile, 128, 256, 32, 128, 4>(A, C, s);
     return launch_product<Tile, 64, 256, 32, 128, 6>(A, C, s);
 }
@@ -734,10 +739,11 @@ hipError_t backward(const ProductArgs &A, const typename GatedBackTile<kEight>::
     // rows a group 815, 952, 1218; 1000 rows (256 of the largest) 148, 130, 168; 400 rows 75, 59,
     // 77; 200 rows 71, 37, 46; 100 rows 66, 34, 32.
     const int64_t rows = A.groups.M / A.groups.G;
-    if (rows >= 256 && !few(A) && ceil_div(A.groups.M, 256) * ceil_div(A.N, 256) >= 512)
+    if (few(A, kFewBackward))
+        return rows >= 128 ? launch_product<Tile, 128, 128, 32, 128, 4, true>(A, C, s)
+                           : launch_product<Tile, 64, 128, 32, 128, 6, true>(A, C, s);
+    if (rows >= 256 && ceil_div(A.groups.M, 256) * ceil_div(A.N, 256) >= 512)
         return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
-    if (few(A) && rows >= 128) return launch_product<Tile, 128, 128, 32, 128, 4, true>(A, C, s);
-    if (few(A)) return launch_product<Tile, 64, 128, 32, 128, 6, true>(A, C, s);
     if (rows >= 128) return launch_product<Tile, 128, 128, 32, 128, 4>(A, C, s);
     return launch_product<Tile, 64, 128, 32, 128, 6>(A, C, s);
 }

@@ -123,7 +123,8 @@ SHAPES = [
     ([200, 97, 128], 700, 640, 8, True, 0, True), ([128, 300], 2048, 384, 0, False, 0, True),
     ([4100], 200, 1500, 4, True, 0, True), ([2500, 1700, 0], 650, 1800, 8, False, 90, True),
     ([5000], 1024, 1280, 0, False, 0, False), ([30000, 22000, 0], 99, 103, 8, False, 0, True),
-    ([26000, 30001], 640, 130, 4, True, 5, True),
+    ([26000, 30001], 640, 130, 4, True, 5, True), ([700, 801], 640, 1500, 4, True, 3, True),
+    ([1501], 400, 1450, 0, False, 0, True), ([100] * 15 + [61], 600, 1401, 8, True, 0, True),
 ]
 
 
@@ -194,7 +195,7 @@ def test_backward(dev, shape, keep):
     assert torch.equal(half, dw.to(BF16))
 
 
-@pytest.mark.parametrize("sizes,inter", [([300, 211], 256), ([3000, 2111], 256), ([3000, 2111], 384)], ids=str)
+@pytest.mark.parametrize("sizes,inter", [([300, 211], 256), ([3000, 2111], 256), ([3500, 2311], 384)], ids=str)
 def test_fused_and_apart_agree(dev, sizes, inter):
     """The block in one product against the grouped product in bf16 and the step on its own: 2^-9 apart before the 8
     bits.  With many rows of many columns they have the same sums, rounded once; else exact sums against those: their
