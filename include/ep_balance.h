@@ -573,6 +573,10 @@ int ep_grouped_wgrad_mixed(const ep_grouped_wgrad_mixed_t *p, ep_stream_t stream
  *                           128: a, zeros, b, zeros, and keep_scale with
  *                           ep_scale_stride(2 * I) bytes a row
  *            rows without an input and past the groups: zeros
+ * Roundings of h (and of q below) are to nearest as in ep_quant_rows, but ties go
+ * away from zero; a and b in 8 bits are rounded as there.  The sums are those of
+ * ep_grouped_matmul; where inter <= 256, k <= 256 or m * inter < 2^21 (below: 2^19)
+ * they are of fp32's precision instead, since single values count more there.
  */
 typedef struct ep_grouped_swiglu {
     const void *x;

@@ -8,6 +8,16 @@
 //             as bf16 (for the weight gradient) and in 8 bits (for the input gradient)
 // Both are one product whose tile becomes the outputs before it leaves the
 // registers: neither [g u] nor d is ever written in 16 bits and read again.
+//
+// What they measured, 8 groups, 65536 rows, hidden 4096, inter 2048, us: forward 943 (two
+// plain products of these sizes 1013; 1.1 PFLOP at 2.33 PFLOP/s; with g and u kept in 8 bits
+// 1016), backward 820 (one plain product 500).  Bound: the forward kernel as the products
+// are (product.h), by waiting in step.  The backward kernel needs 576 for d and the
+// arithmetic, and 805 MB more of HBM traffic than the product (bf16 and 8-bit gradients out,
+// g and u in), which comes in bursts at a tile's end while no wave multiplies: one
+// workgroup a CU has all registers.  Two of 128 x 128, which could take turns, load their
+// operands twice as often and need 952; starting workgroups apart and stores that pass the
+// caches by gained nothing.
 #include <utility>
 
 #include "product.h"
@@ -20,8 +30,9 @@ enum Keep { kNone, kSixteen, kEight };
 // ---- a lane's 16 values of a 32 x 32 fragment ----
 // Value e belongs to column 8 (e / 4) + 4 (lane / 32) + e % 4 of the fragment's
 // row lane % 32.  Memory takes rows in pieces of 64 bytes best, 16 from each of 4
-// lanes (pieces of 32 cost twice the requests: the backward kernel's stores took
-// NEW), so two swaps bring them together:
+// lanes (in pieces of 32 the backward kernel's bf16 stores cost 145 us over the 580 of
+// the kernel without them, at 65536 x 2048 and K = 4096; so they cost 118), and two
+// swaps bring them together:
 //   between the halves of the wave, after which a lane has 16 bytes in a row;
 //   between rows of 16 lanes, of two such vectors that lie side by side in memory: one
 //   then has both of rows 0 .. 15 of the fragment, the other both of rows 16 .. 31.
@@ -719,7 +730,10 @@ hipError_t forward(const ProductArgs &A, const typename GatedTile<kNone>::Args &
     // mostly fill them.  Measured, us for 8 groups, hidden 4096, inter 2048 with tiles of
     // 256, 128, 64 rows: 1000 rows a group 158, 175, 243; 400 rows 62, 74, 109; 200 rows
     // 52, 41, 59; 100 rows 48, 34, 32.  5003 rows in 3 groups of 1999 x 1003 (160 tiles of
-    // 256): 32, 39, 46; 3001 rows in 5 of 1000 x 777 (84): 21, 15, 21.
+    // 256): 32, 39, 46; 3001 rows in 5 of 1000 x 777 (84): 21, 15, 21.  A row or two a group of
+    // hidden 4096, inter 2048 (128 tiles, 134 MB of weights from HBM) take 42 us; tiles of 32
+    // rows with 6 or 8 stages 40 to 45, and 8-bit sums 40: a CU takes in 26 to 32 bytes a ns,
+    // and half of them have no tile.
     const int64_t rows = A.groups.M / A.groups.G;
     if (few(A, kFewForward))
         return rows >= 128 ? launch_product<Tile, 128, 256, 32, 128, 4, true>(A, C, s)

@@ -22,6 +22,13 @@
 // and stores 16 bytes.  Rows past the group's end and columns past the matrix
 // are fetched from a block of zeros, so that neighbours' values (which may be
 // infinite) never enter.
+//
+// Rows that are held in 8 bits (ep_grouped_wgrad_mixed) are widened to bf16 in the
+// workspace first, which holds them exactly, by a kernel of its own: 65536 rows in 8
+// groups, N = 4096, K = 4096 take 2100 us so, the bf16 form with plain rows 1945.  Opened
+// inside the loop, where every tile of N opens its rows of x again and they pass
+// registers on their way into LDS, 2440.  A list of rows (either operand, or both) is
+// read 128 places ahead into LDS and costs 8 % of the loop.
 #include "columns.h"
 
 namespace ep {
