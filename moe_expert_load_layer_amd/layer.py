@@ -372,13 +372,13 @@ def _places(t: Optional[torch.Tensor], name: str) -> int:
     return t.shape[0]
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, device, stream):
-    """(address, bytes) of the workspace that is given, or of a new one."""
+def _workspace(ws: Optional[torch.Tensor], need: int, device, stream) -> torch.Tensor:
+    """The workspace that is given, or a new one; the caller holds it until its call, or another output takes its place."""
     if ws is None:
         ws = _held(torch.empty(max(16, need), dtype=torch.uint8, device=device), stream)
     elif not (ws.is_cuda and ws.is_contiguous()):
         raise EPBalanceError("ws must be a contiguous device tensor")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws
 
 
 def ep_wgrad_mixed_workspace_bytes(rows: int, cols: int) -> int:
@@ -420,7 +420,8 @@ def ep_grouped_wgrad_mixed(dy: torch.Tensor, x: torch.Tensor, x_scale: torch.Ten
                      None if dy_rows is None else dy_rows.data_ptr(), None if x_rows is None else x_rows.data_ptr(),
                      rows_div, G, None if offsets is None else offsets.data_ptr(), M, N, K, None, out.data_ptr(), None,
                      out.stride(0), 0)
-    p.ws, p.ws_bytes = _workspace(ws, ep_wgrad_mixed_workspace_bytes(x.shape[0], K), dy.device, stream)
+    ws = _workspace(ws, ep_wgrad_mixed_workspace_bytes(x.shape[0], K), dy.device, stream)
+    p.ws, p.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     if layout is not None:
         p.layout = ctypes.pointer(layout.c)
         slot_out = _gradient(slot_out, (layout.num_spare, N, K), dy.device, "slot_out", stream)
@@ -548,7 +549,8 @@ def ep_grouped_swiglu_backward(dy: torch.Tensor, dy_scale: torch.Tensor, down: t
         grad_weights = _out(grad_weights, weights_dtype, (pairs,), dy.device, "grad_weights", stream)
         p.weights, p.grad_weights, p.grad_weights_dtype = weights.data_ptr(), grad_weights.data_ptr(), _FLOATS[weights_dtype]
         p.pos, p.pairs = None if pos is None else pos.data_ptr(), pairs
-        p.ws, p.ws_bytes = _workspace(ws, ep_swiglu_backward_workspace_bytes(M, I), dy.device, stream)
+        ws = _workspace(ws, ep_swiglu_backward_workspace_bytes(M, I), dy.device, stream)
+        p.ws, p.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     elif pos is not None or grad_weights is not None:
         raise EPBalanceError("grad_weights and pos need weights")
     if layout is not None:

@@ -173,3 +173,68 @@ def test_rows_apart_are_the_same_rows_where_halves_are_whole_blocks(dev):
     both = S.matrix(a.back.both_t[1], a.back.both_t_scale[1], 256)
     assert torch.equal(both[:, :128].t(), S.matrix(a.experts.gate[1], a.experts.gate_scale[1], 256))
     assert np.prod(a.back.both_t.shape[1:]) == 2 * 128 * 256
+
+
+def _flat(r, g):
+    return [r["out"], r["h"][0].view(torch.uint8), r["kept"][0], g["x"], g["logits"], g["gate_up"], g["down"]]
+
+
+def test_a_captured_step_replays_as_an_eager_one(dev):
+    """The whole step in one graph, replayed over other inputs with eager steps and synchronizations between."""
+    s = Setup(dev, 16, 4, 1, 40, 256, 128)
+    s.step(2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = _flat(*s.step(2))
+    gen = torch.Generator(device=dev).manual_seed(5)
+    for i in range(4):
+        s.x.copy_(torch.randn(s.x.shape, generator=gen, device=dev))
+        s.logits.copy_(torch.randn(s.logits.shape, generator=gen, device=dev))
+        s.dout.copy_(torch.randn(s.dout.shape, generator=gen, device=dev))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        for a, b in zip(got, _flat(*s.step(2))):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+
+
+@pytest.mark.parametrize("tokens,k,spare", [(1, 1, 0), (1, 2, 1), (3, 4, 2)])
+def test_few_tokens(dev, tokens, k, spare):
+    """A rank's single token, one expert each, no spare slots; the experts that got nothing have gradients of 0."""
+    s = Setup(dev, 8, 2, spare, tokens, 128, 256)
+    r, g = s.step(k)
+    used = torch.zeros(8, dtype=torch.bool, device=dev)
+    used[r["ids"].long().flatten()] = True
+    for name in ("gate_up", "down"):
+        assert torch.isfinite(g[name]).all() and (g[name][~used] == 0).all()
+        assert (g[name][used].flatten(1).abs().sum(1) > 0).all()
+    assert torch.isfinite(g["x"].float()).all() and torch.isfinite(g["logits"]).all()
+    assert (g["x"].float().abs().sum(1) > 0).all()
+
+
+def test_a_new_workspace_is_no_output(dev, monkeypatch):
+    """The workspace that a call makes is apart from all it writes, also where their sizes are alike."""
+    from moe_expert_load_layer_amd import layer as module
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            return getattr(ep.lib(), name)
+
+        def ep_grouped_wgrad_mixed(self, p, stream):
+            q = p._obj
+            seen.append([(q.ws, q.ws_bytes), (q.out, 8 * 64 * 128 * 4), (q.slot_out, 2 * 64 * 128 * 4)])
+            return 0
+
+    monkeypatch.setattr(module, "lib", Library)
+    lay = ep.Layout.create(8, [4, 4], list(range(8)), [1, 1], device=dev)
+    for rows in (64, 256, 1024):        # 256: the workspace is as large as the spare slots' gradients, 1024: as the others'
+        x, scale = ep.ep_quant_rows(torch.ones((rows, 128), dtype=BF16, device=dev))
+        offsets = torch.full((11,), rows, dtype=torch.int32, device=dev)
+        ep.ep_grouped_wgrad_mixed(torch.ones((rows, 64), dtype=BF16, device=dev), x, scale, offsets, layout=lay)
+    for ranges in seen:
+        for i, (a, n) in enumerate(ranges):
+            for b, m in ranges[i + 1:]:
+                assert a + n <= b or b + m <= a
+    assert len(seen) == 3
