@@ -732,8 +732,9 @@ hipError_t forward(const ProductArgs &A, const typename GatedTile<kNone>::Args &
     // 52, 41, 59; 100 rows 48, 34, 32.  5003 rows in 3 groups of 1999 x 1003 (160 tiles of
     // 256): 32, 39, 46; 3001 rows in 5 of 1000 x 777 (84): 21, 15, 21.  A row or two a group of
     // hidden 4096, inter 2048 (128 tiles, 134 MB of weights from HBM) take 42 us; tiles of 32
-    // rows with 6 or 8 stages 40 to 45, and 8-bit sums 40: a CU takes in 26 to 32 bytes a ns,
-    // and half of them have no tile.
+    // rows with 6 or 8 stages 40 to 45, and 8-bit sums 40.  A kernel that only loads these
+    // tiles takes 34 (27 in pieces of 1 KiB a row, which the loop has no use for), and no less
+    // with more in flight.
     const int64_t rows = A.groups.M / A.groups.G;
     if (few(A, kFewForward))
         return rows >= 128 ? launch_product<Tile, 128, 256, 32, 128, 4, true>(A, C, s)
