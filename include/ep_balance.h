@@ -574,9 +574,14 @@ int ep_grouped_wgrad_mixed(const ep_grouped_wgrad_mixed_t *p, ep_stream_t stream
  *                           ep_scale_stride(2 * I) bytes a row
  *            rows without an input and past the groups: zeros
  * Roundings of h (and of q below) are to nearest as in ep_quant_rows, but ties go
- * away from zero; a and b in 8 bits are rounded as there.  The sums are those of
- * ep_grouped_matmul; where inter <= 256, k <= 256 or m * inter < 2^21 (below: 2^19)
- * they are of fp32's precision instead, since single values count more there.
+ * away from zero; a and b in 8 bits are rounded as there.
+ *   sums8    0: the sums are of fp32's precision, so that few values are rounded to
+ *            8 bits another way than the sums' exact values.  1: those of
+ *            ep_grouped_matmul, in little more than half the time for many rows; they
+ *            are off by up to 6e-5 of a result where some columns of x are much larger
+ *            than others, and send one value in 300 the other way, by a sixteenth of it
+ * A row's outputs do not depend on the other rows.  (The gradient below: sums of fp32's
+ * precision where inter <= 256, k <= 256 or m * inter < 2^19, else ep_grouped_matmul's.)
  */
 typedef struct ep_grouped_swiglu {
     const void *x;
@@ -595,6 +600,7 @@ typedef struct ep_grouped_swiglu {
     int32_t keep_dtype;
     void *keep;
     uint8_t *keep_scale;
+    int32_t sums8;
 } ep_grouped_swiglu_t;
 int ep_grouped_swiglu(const ep_grouped_swiglu_t *p, ep_stream_t stream);
 

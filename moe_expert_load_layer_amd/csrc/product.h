@@ -193,8 +193,8 @@ constexpr int waves_a_simd(int BM, int BN, int WM, int WN, int kStages) {
 //   tail(...)   the rows past the last group, by all threads
 //
 // kExact: each operand opened to bf16 and multiplied by the 16-bit instruction, whose
-// sums are fp32's, at half the rate and with 16 conversions a fragment; for products
-// that wait for their weights anyway, where the sums are rounded to 8 bits again.
+// sums are fp32's, at half the rate and with 16 conversions a fragment; for sums that are
+// rounded to 8 bits again.
 template <class Store, int BM, int BN, int WM, int WN, int kStages, bool kChained, bool kExact>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave, waves_a_simd(BM, BN, WM, WN, kStages)) void product_kernel(const ProductArgs A,
                                                                                    const typename Store::Args B) {

@@ -9,10 +9,11 @@
 // Both are one product whose tile becomes the outputs before it leaves the
 // registers: neither [g u] nor d is ever written in 16 bits and read again.
 //
-// What they measured, 8 groups, 65536 rows, hidden 4096, inter 2048, us: forward 943 (two
-// plain products of these sizes 1013; 1.1 PFLOP at 2.33 PFLOP/s; with g and u kept in 8 bits
-// 1016), backward 820 (one plain product 500).  Bound: the forward kernel as the products
-// are (product.h), by waiting in step.  The backward kernel needs 576 for d and the
+// What they measured, 8 groups, 65536 rows, hidden 4096, inter 2048, us: forward 1720 (2.2
+// TFLOP at 1.28 PFLOP/s by the 16-bit instruction, which bounds it; with g and u kept in 8
+// bits 1770), with the 8-bit sums 943 (two plain products of these sizes 1013; 2.33 PFLOP/s,
+// bound as they are, by waiting in step; 1016), backward 820 (one plain product 500).  The
+// backward kernel needs 576 for d and the
 // arithmetic, and 805 MB more of HBM traffic than the product (bf16 and 8-bit gradients out,
 // g and u in), which comes in bursts at a tile's end while no wave multiplies: one
 // workgroup a CU has all registers.  Two of 128 x 128, which could take turns, load their
@@ -705,44 +706,48 @@ __global__ __launch_bounds__(kDotThreads) void pair_dots_kernel(const float *__r
     else static_cast<float *>(out)[i] = s;
 }
 
-// Whether single values count among those that come out, because they are few, or a
-// row has few, or a sum has few terms that could make up for one another: a sum of
-// 8-bit products that is off by 2^-14 sends one in 300 of the values rounded to 8 bits
-// the other way, by a sixteenth of itself, which thousands of others outweigh and a few
-// large ones do not.  These take the exact sums.  Over 1000 random shapes, some rows and
-// columns of them much larger than others, the error to 64 bits passed 5e-3 in 5 % of
-// the shapes without them (1.7e-3 is the bf16 outputs' own, 2.6e-3 the rule).  The forward
-// kernel's values go on into everything, so it takes them up to 4 times as many.
+// The sums decide which way values are rounded to 8 bits, steps of a sixteenth: one that
+// is off by the 8-bit instruction's 2^-14 sends one value in 300 the other way, and where
+// a few rows or values carry an output's norm, one is seen there.  So the forward kernel
+// opens its operands (product.h) and adds in fp32 whatever the sizes, and a row's outputs
+// do not depend on how many others there are.  The 8-bit sums are the caller's choice.
 //
-// Cost, us forward and backward: 65536 rows, 2048 x 200 180 + 110 against 107 + 86; 30340 rows,
-// 754 x 143 41 + 40 against 27 + 35; 8 rows of 8 groups, 4096 x 2048 34 against 28 forward;
-// 640 rows of 8 groups, 4096 x 1024 36 against 30.
-bool few(const ProductArgs &A, int64_t values) {
-    return A.N <= 256 || A.kb <= 2 || (int64_t)A.groups.M * A.N < values;
+// Error of the block's output y against 64 bits, exact and 8-bit sums: 65536 rows, 4096 x
+// 2048 1.66e-3 (what its rounding to bf16 gives) and 2.5e-3, 3001 rows, 1000 x 777 1.66e-3
+// and 2.0 to 3.0e-3 over four seeds (up to 9e-3 seen).  us for 8 groups of hidden 4096,
+// inter 2048, exact and 8-bit: 8192 rows a group 1720 and 990 (1.28 PFLOP/s of a library
+// product's 1.19 to 1.54 in bf16), 1000 rows 283 and 155, 400 rows 110 and 62, 100 rows 39
+// and 32, one row 35 and 28.
+//
+// The backward kernel: where single values count among those that come out, because they
+// are few, or a row has few, or a sum has few terms.
+bool few(const ProductArgs &A) {
+    return A.N <= 256 || A.kb <= 2 || (int64_t)A.groups.M * A.N < (int64_t)1 << 19;
 }
-constexpr int64_t kFewForward = 1 << 21, kFewBackward = 1 << 19;
 
-template <Keep kKeep>
+template <Keep kKeep, bool kExact>
 hipError_t forward(const ProductArgs &A, const typename GatedTile<kNone>::Args &B, hipStream_t s) {
     typedef GatedTile<kKeep> Tile;
     const typename Tile::Args C{B.up, B.weights, B.h, B.h_scale, B.kept, B.kept_scale, B.ib, B.hs, B.ks};
     // 256 rows where tiles of 128 would take the 256 CUs more than one round, and groups
     // mostly fill them.  Measured, us for 8 groups, hidden 4096, inter 2048 with tiles of
-    // 256, 128, 64 rows: 1000 rows a group 158, 175, 243; 400 rows 62, 74, 109; 200 rows
-    // 52, 41, 59; 100 rows 48, 34, 32.  5003 rows in 3 groups of 1999 x 1003 (160 tiles of
-    // 256): 32, 39, 46; 3001 rows in 5 of 1000 x 777 (84): 21, 15, 21.  A row or two a group of
-    // hidden 4096, inter 2048 (128 tiles, 134 MB of weights from HBM) take 42 us; tiles of 32
-    // rows with 6 or 8 stages 40 to 45, and 8-bit sums 40.  A kernel that only loads these
-    // tiles takes 34 (27 in pieces of 1 KiB a row, which the loop has no use for), and no less
-    // with more in flight.
+    // 256, 128, 64 rows: 1000 rows a group 283, 285, 307; 400 rows 110, 126, 142; 200 rows
+    // 91, 63, 74; 100 rows 86, 54, 39.  5003 rows in 3 groups of 1999 x 1003 (160 tiles of
+    // 256): 50, 61, 58; 3001 rows in 5 of 1000 x 777 (84): 32, 22, 29.  With 8-bit sums:
+    // 158, 175, 243; 62, 74, 109; 52, 41, 59; 48, 34, 32; 32, 39, 46; 21, 15, 21.  A row or
+    // two a group of hidden 4096, inter 2048 (128 tiles, 134 MB of weights from HBM) take 42
+    // us; tiles of 32 rows with 6 or 8 stages 40 to 45, and 8-bit sums 40.  A kernel that
+    // only loads these tiles takes 34 (27 in pieces of 1 KiB a row, which the loop has no use
+    // for), and no less with more in flight.
     const int64_t rows = A.groups.M / A.groups.G;
-    if (few(A, kFewForward))
-        return rows >= 128 ? launch_product<Tile, 128, 256, 32, 128, 4, true>(A, C, s)
-                           : launch_product<Tile, 64, 256, 32, 128, 6, true>(A, C, s);
     if (rows >= 256 && ceil_div(A.groups.M, 256) * ceil_div(A.N, kScaleBlock) > 128)
-        return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
-    if (rows >= 128) return launch_product<Tile, 128, 256, 32, 128, 4>(A, C, s);
-    return launch_product<Tile, 64, 256, 32, 128, 6>(A, C, s);
+        return launch_product<Tile, 256, 256, 64, 128, 4, kExact>(A, C, s);
+    if (rows >= 128) return launch_product<Tile, 128, 256, 32, 128, 4, kExact>(A, C, s);
+    return launch_product<Tile, 64, 256, 32, 128, 6, kExact>(A, C, s);
+}
+template <Keep kKeep>
+hipError_t forward(bool sums8, const ProductArgs &A, const typename GatedTile<kNone>::Args &B, hipStream_t s) {
+    return sums8 ? forward<kKeep, false>(A, B, s) : forward<kKeep, true>(A, B, s);
 }
 
 template <Keep kKeep>
@@ -754,7 +759,7 @@ hipError_t backward(const ProductArgs &A, const typename GatedBackTile<kEight>::
     // rows a group 815, 952, 1218; 1000 rows (256 of the largest) 148, 130, 168; 400 rows 75, 59,
     // 77; 200 rows 71, 37, 46; 100 rows 66, 34, 32.
     const int64_t rows = A.groups.M / A.groups.G;
-    if (few(A, kFewBackward))
+    if (few(A))
         return rows >= 128 ? launch_product<Tile, 128, 128, 32, 128, 4, true>(A, C, s)
                            : launch_product<Tile, 64, 128, 32, 128, 6, true>(A, C, s);
     if (rows >= 256 && ceil_div(A.groups.M, 256) * ceil_div(A.N, 256) >= 512)
@@ -796,7 +801,8 @@ extern "C" int ep_grouped_swiglu(const ep_grouped_swiglu_t *p, ep_stream_t strea
     if (!p) return EP_ERR_INVALID_ARG;
     const ProductShape shape{p->x, p->x_scale, p->x_rows, p->rows, p->rows_div, p->groups, p->offsets, p->m, p->inter,
                              p->k, p->weights, p->weights_count};
-    if (!product_sizes_ok(shape) || (p->keep && !keep_dtype(p->keep_dtype))) return EP_ERR_INVALID_ARG;
+    if (!product_sizes_ok(shape) || (p->keep && !keep_dtype(p->keep_dtype)) || (p->sums8 != 0 && p->sums8 != 1))
+        return EP_ERR_INVALID_ARG;
     if (p->m == 0) return EP_OK;
     const bool slots = p->slot_gate.data && p->slot_gate.scale && p->slot_up.data && p->slot_up.scale;
     ProductArgs A;
@@ -815,8 +821,9 @@ extern "C" int ep_grouped_swiglu(const ep_grouped_swiglu_t *p, ep_stream_t strea
         p->weights, p->h, p->h_scale, p->keep, p->keep_scale, ib, (int32_t)ep_scale_stride(p->inter),
         (int32_t)ep_scale_stride((int64_t)2 * ib * kScaleBlock)};
     const hipStream_t s = to_stream(stream);
-    if (!p->keep) return rc_of(forward<kNone>(A, B, s));
-    return rc_of(p->keep_dtype == EP_DTYPE_BF16 ? forward<kSixteen>(A, B, s) : forward<kEight>(A, B, s));
+    const bool sums8 = p->sums8 != 0;
+    if (!p->keep) return rc_of(forward<kNone>(sums8, A, B, s));
+    return rc_of(p->keep_dtype == EP_DTYPE_BF16 ? forward<kSixteen>(sums8, A, B, s) : forward<kEight>(sums8, A, B, s));
 }
 
 extern "C" size_t ep_swiglu_backward_workspace_bytes(int64_t m, int64_t inter) {

@@ -48,7 +48,8 @@ class _CSwiglu(ctypes.Structure):
     _fields_ = [("x", _vp), ("x_scale", _vp), ("x_rows", _i64), ("rows", _vp), ("rows_div", _i32), ("groups", _i32),
                 ("offsets", _vp), ("m", _i64), ("inter", _i64), ("k", _i64), ("gate", _CMatrix), ("up", _CMatrix),
                 ("slot_gate", _CMatrix), ("slot_up", _CMatrix), ("layout", ctypes.POINTER(_CLayout)), ("weights", _vp),
-                ("weights_count", _i64), ("h", _vp), ("h_scale", _vp), ("keep_dtype", _i32), ("keep", _vp), ("keep_scale", _vp)]
+                ("weights_count", _i64), ("h", _vp), ("h_scale", _vp), ("keep_dtype", _i32), ("keep", _vp), ("keep_scale", _vp),
+                ("sums8", _i32)]
 
 
 class _CSwigluBackward(ctypes.Structure):
@@ -450,13 +451,15 @@ def ep_grouped_swiglu(x: torch.Tensor, x_scale: torch.Tensor, gate: torch.Tensor
                       rows: Optional[torch.Tensor] = None, rows_div: int = 1, weights: Optional[torch.Tensor] = None,
                       keep: Optional[torch.dtype] = None, layout: Optional[Layout] = None, slot_gate=None,
                       slot_gate_scale=None, slot_up=None, slot_up_scale=None, h=None, h_scale=None, kept=None,
-                      kept_scale=None, stream=None):
+                      kept_scale=None, stream=None, sums8: bool = False):
     """h[i] = w_i silu(gate_g x[r(i)]) * (up_g x[r(i)]) in 8 bits, for the rows i of group g, in one product.
 
     x, x_scale from ep_quant_rows, gate and up [G][I][K up to 128] with the scales of ep_quant_blocks; offsets, rows,
     rows_div and layout as for ep_grouped_matmul.  weights float32, one for each pair that rows may name (a pair past
     them has no input; without rows: [M]); None: 1.  keep: None, or the type in which the two products are kept for
     ep_grouped_swiglu_backward, torch.bfloat16 ([M][2 I]) or torch.float8_e4m3fn ([M][2 * (I up to 128)] and scales).
+    sums8: the 8-bit instruction's sums, as ep_grouped_matmul has them, in place of fp32's: little more than half the
+    time for many rows, but one value in 300 is rounded to 8 bits the other way.
     Returns (h, h_scale, kept, kept_scale), the last two None where there are none."""
     if x.dim() != 2 or gate.dim() != 3 or x.shape[1] % 128 or x.shape[1] != gate.shape[2]:
         raise EPBalanceError(f"x [rows][k] and gate [groups][inter][k] must share k, a multiple of 128: got "
@@ -489,7 +492,7 @@ def ep_grouped_swiglu(x: torch.Tensor, x_scale: torch.Tensor, gate: torch.Tensor
                  _matrix(up, up_scale, I, K, "up"), _CMatrix(), _CMatrix(), None,
                  None if weights is None else weights.data_ptr(), count, h.data_ptr(), h_scale.data_ptr(),
                  EP_DTYPE_FP8 if keep is _FP8 else EP_DTYPE_BF16, None if kept is None else kept.data_ptr(),
-                 None if kept_scale is None else kept_scale.data_ptr())
+                 None if kept_scale is None else kept_scale.data_ptr(), int(bool(sums8)))
     if layout is not None:
         p.layout = ctypes.pointer(layout.c)
         if layout.num_spare:
@@ -725,13 +728,13 @@ def run_layer(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layout, exp
 
 def run_layer_train(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layout, experts: ExpertRows,
                     slots: ExpertRows, bias=None, num_groups: int = 1, topk_groups: int = 1, scale: float = 1.0,
-                    keep: torch.dtype = _FP8):
+                    keep: torch.dtype = _FP8, sums8: bool = False):
     """run_layer's layer in a training step: returns a dict with out bf16 [tokens][H], ids, weights, plan, status,
     offsets, pos, src, and what run_layer_backward needs besides.
 
     What is kept of the activations for it: x and the weighted silu(g) u in 8 bits, as the products take them, and g
     and u in `keep` (torch.float8_e4m3fn or torch.bfloat16).  experts and slots need gate and up with their own scales
-    (ExpertRows)."""
+    (ExpertRows).  sums8: as in ep_grouped_swiglu."""
     if x.dim() != 2 or logits.dim() != 2 or x.shape[0] != logits.shape[0]:
         raise EPBalanceError(f"x [tokens][hidden] and logits [tokens][experts] must have the same tokens, got "
                              f"{tuple(x.shape)} and {tuple(logits.shape)}")
@@ -748,7 +751,7 @@ def run_layer_train(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layou
         xq, xs, experts.gate, experts.gate_scale, experts.up, experts.up_scale, offsets[0], rows=src[0], rows_div=k,
         weights=weights.view(-1), keep=keep, layout=layout, slot_gate=slots.gate if spare else None,
         slot_gate_scale=slots.gate_scale if spare else None, slot_up=slots.up if spare else None,
-        slot_up_scale=slots.up_scale if spare else None)
+        slot_up_scale=slots.up_scale if spare else None, sums8=sums8)
     y = ep_grouped_matmul(h, hs, experts.down, experts.down_scale, offsets[0], layout=layout,
                           slot_w=slots.down if spare else None, slot_w_scale=slots.down_scale if spare else None)
     out = ep_moe_combine(y, pos.view(-1, k), torch.ones_like(weights))
