@@ -580,8 +580,7 @@ int ep_grouped_wgrad_mixed(const ep_grouped_wgrad_mixed_t *p, ep_stream_t stream
  *            ep_grouped_matmul, in little more than half the time for many rows; they
  *            are off by up to 6e-5 of a result where some columns of x are much larger
  *            than others, and send one value in 300 the other way, by a sixteenth of it
- * A row's outputs do not depend on the other rows.  (The gradient below: sums of fp32's
- * precision where inter <= 256, k <= 256 or m * inter < 2^19, else ep_grouped_matmul's.)
+ * A row's outputs do not depend on the other rows.
  */
 typedef struct ep_grouped_swiglu {
     const void *x;
@@ -618,10 +617,10 @@ int ep_grouped_swiglu(const ep_grouped_swiglu_t *p, ep_stream_t stream);
  *            that gives the input gradient, with the matrices [groups][hidden][2 * I];
  *            or NULL
  *   grad_weights  device float or bf16 (grad_weights_dtype) [pairs], or NULL: dw at
- *            i = pos[pair], 0 where pos is outside [0, m); pos NULL: dw_i, pairs == m.
- *            d keeps about 16 bits (see ep_grouped_matmul's product), so does dw
+ *            i = pos[pair], 0 where pos is outside [0, m); pos NULL: dw_i, pairs == m
  *   ws       with grad_weights: ep_swiglu_backward_workspace_bytes(m, inter) bytes, 16-byte
  *            aligned; no state between calls, calls in flight at once need their own
+ *   sums8    as there; with 1, d and so dw keep about 16 bits
  * Every element of the outputs is written; rows without a dy are zeros.
  */
 typedef struct ep_grouped_swiglu_backward {
@@ -648,6 +647,7 @@ typedef struct ep_grouped_swiglu_backward {
     int64_t pairs;
     void *ws;
     size_t ws_bytes;
+    int32_t sums8;
 } ep_grouped_swiglu_backward_t;
 size_t ep_swiglu_backward_workspace_bytes(int64_t m, int64_t inter);
 int ep_grouped_swiglu_backward(const ep_grouped_swiglu_backward_t *p, ep_stream_t stream);

@@ -12,8 +12,8 @@
 // What they measured, 8 groups, 65536 rows, hidden 4096, inter 2048, us: forward 1720 (2.2
 // TFLOP at 1.28 PFLOP/s by the 16-bit instruction, which bounds it; with g and u kept in 8
 // bits 1770), with the 8-bit sums 943 (two plain products of these sizes 1013; 2.33 PFLOP/s,
-// bound as they are, by waiting in step; 1016), backward 820 (one plain product 500).  The
-// backward kernel needs 576 for d and the
+// bound as they are, by waiting in step; 1016), backward 1214 and 820 (one plain product
+// 500).  With those the backward kernel needs 576 for d and the
 // arithmetic, and 805 MB more of HBM traffic than the product (bf16 and 8-bit gradients out,
 // g and u in), which comes in bursts at a tile's end while no wave multiplies: one
 // workgroup a CU has all registers.  Two of 128 x 128, which could take turns, load their
@@ -719,12 +719,10 @@ __global__ __launch_bounds__(kDotThreads) void pair_dots_kernel(const float *__r
 // product's 1.19 to 1.54 in bf16), 1000 rows 283 and 155, 400 rows 110 and 62, 100 rows 39
 // and 32, one row 35 and 28.
 //
-// The backward kernel: where single values count among those that come out, because they
-// are few, or a row has few, or a sum has few terms.
-bool few(const ProductArgs &A) {
-    return A.N <= 256 || A.kb <= 2 || (int64_t)A.groups.M * A.N < (int64_t)1 << 19;
-}
-
+// The backward kernel the same, since its gradients are rounded to 8 bits again and dw adds
+// up terms that cancel.  Error of the input gradient formed from q 1.66e-3 and 1.9e-3
+// (with the same g and u), 820 us with the 8-bit sums for 8192 rows a group, 1214 with these;
+// 1000 rows 167 and 142, 400 rows 78 and 59, 100 rows 46 and 32.
 template <Keep kKeep, bool kExact>
 hipError_t forward(const ProductArgs &A, const typename GatedTile<kNone>::Args &B, hipStream_t s) {
     typedef GatedTile<kKeep> Tile;
@@ -750,22 +748,27 @@ hipError_t forward(bool sums8, const ProductArgs &A, const typename GatedTile<kN
     return sums8 ? forward<kKeep, false>(A, B, s) : forward<kKeep, true>(A, B, s);
 }
 
-template <Keep kKeep>
+template <Keep kKeep, bool kExact>
 hipError_t backward(const ProductArgs &A, const typename GatedBackTile<kEight>::Args &B, hipStream_t s) {
     typedef GatedBackTile<kKeep> Tile;
     const typename Tile::Args C{B.weights, B.kept, B.kept_scale, B.dgu, B.q, B.q_scale, B.dots, B.ib, B.qs};
-    // The largest tiles where every CU has two, else two workgroups a CU.  Measured, us for
-    // 8 groups, hidden 4096, inter 2048 with tiles of 256 x 256, 128 x 128, 64 x 128: 8192
-    // rows a group 815, 952, 1218; 1000 rows (256 of the largest) 148, 130, 168; 400 rows 75, 59,
-    // 77; 200 rows 71, 37, 46; 100 rows 66, 34, 32.
+    // Two workgroups a CU; with 8-bit sums the largest tiles where every CU has two.
+    // Measured, us for 8 groups, hidden 4096, inter 2048 with tiles of 256 x 256, 128 x 128,
+    // 64 x 128: 8192 rows a group 1135, 1214, 1425; 4000 rows 612, 602, 696; 1000 rows 222,
+    // 167, 208; 400 rows 110, 78, 88; 200 rows 106, 49, 52; 100 rows 103, 46, 46.  65536 rows in
+    // 16 groups of 512 x 1024: 246, 222, 314.  With 8-bit sums, 8192 rows a group: 815, 952,
+    // 1218; 1000 rows (256 of the largest) 148, 130, 168; 400 rows 75, 59, 77; 200 rows 71, 37,
+    // 46; 100 rows 66, 34, 32.
     const int64_t rows = A.groups.M / A.groups.G;
-    if (few(A))
-        return rows >= 128 ? launch_product<Tile, 128, 128, 32, 128, 4, true>(A, C, s)
-                           : launch_product<Tile, 64, 128, 32, 128, 6, true>(A, C, s);
-    if (rows >= 256 && ceil_div(A.groups.M, 256) * ceil_div(A.N, 256) >= 512)
-        return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
-    if (rows >= 128) return launch_product<Tile, 128, 128, 32, 128, 4>(A, C, s);
-    return launch_product<Tile, 64, 128, 32, 128, 6>(A, C, s);
+    if constexpr (!kExact)
+        if (rows >= 256 && ceil_div(A.groups.M, 256) * ceil_div(A.N, 256) >= 512)
+            return launch_product<Tile, 256, 256, 64, 128, 4>(A, C, s);
+    if (rows >= 128) return launch_product<Tile, 128, 128, 32, 128, 4, kExact>(A, C, s);
+    return launch_product<Tile, 64, 128, 32, 128, 6, kExact>(A, C, s);
+}
+template <Keep kKeep>
+hipError_t backward(bool sums8, const ProductArgs &A, const typename GatedBackTile<kEight>::Args &B, hipStream_t s) {
+    return sums8 ? backward<kKeep, false>(A, B, s) : backward<kKeep, true>(A, B, s);
 }
 
 // what a matrix argument becomes
@@ -835,7 +838,8 @@ extern "C" int ep_grouped_swiglu_backward(const ep_grouped_swiglu_backward_t *p,
     if (!p) return EP_ERR_INVALID_ARG;
     const ProductShape shape{p->dy, p->dy_scale, p->dy_rows, p->rows, p->rows_div, p->groups, p->offsets, p->m,
                              p->inter, p->k, p->weights, p->weights_count};
-    if (!product_sizes_ok(shape) || !keep_dtype(p->keep_dtype)) return EP_ERR_INVALID_ARG;
+    if (!product_sizes_ok(shape) || !keep_dtype(p->keep_dtype) || (p->sums8 != 0 && p->sums8 != 1))
+        return EP_ERR_INVALID_ARG;
     if (p->grad_weights && (!float_dtype(p->grad_weights_dtype) || p->pairs < 0 || p->pairs > (int64_t)1 << 38 ||
                             !is_aligned(p->grad_weights, p->grad_weights_dtype == EP_DTYPE_BF16 ? 2 : 4) ||
                             !is_aligned(p->pos, 4) || (!p->pos && p->pairs != p->m)))
@@ -858,7 +862,9 @@ extern "C" int ep_grouped_swiglu_backward(const ep_grouped_swiglu_backward_t *p,
                                             p->q_scale, p->grad_weights ? static_cast<float *>(p->ws) : nullptr, ib,
                                             (int32_t)ep_scale_stride((int64_t)2 * ib * kScaleBlock)};
         const hipStream_t s = to_stream(stream);
-        const hipError_t e = p->keep_dtype == EP_DTYPE_BF16 ? backward<kSixteen>(A, B, s) : backward<kEight>(A, B, s);
+        const bool sums8 = p->sums8 != 0;
+        const hipError_t e = p->keep_dtype == EP_DTYPE_BF16 ? backward<kSixteen>(sums8, A, B, s)
+                                                            : backward<kEight>(sums8, A, B, s);
         if (e != hipSuccess) return EP_ERR_HIP;
     }
     if (p->grad_weights && p->pairs > 0) {

@@ -57,7 +57,8 @@ class _CSwigluBackward(ctypes.Structure):
                 ("offsets", _vp), ("m", _i64), ("inter", _i64), ("k", _i64), ("down", _CMatrix), ("slot_down", _CMatrix),
                 ("layout", ctypes.POINTER(_CLayout)), ("weights", _vp), ("weights_count", _i64), ("keep_dtype", _i32),
                 ("keep", _vp), ("keep_scale", _vp), ("grad", _vp), ("q", _vp), ("q_scale", _vp), ("grad_weights", _vp),
-                ("grad_weights_dtype", _i32), ("pos", _vp), ("pairs", _i64), ("ws", _vp), ("ws_bytes", _sz)]
+                ("grad_weights_dtype", _i32), ("pos", _vp), ("pairs", _i64), ("ws", _vp), ("ws_bytes", _sz),
+                ("sums8", _i32)]
 
 
 class _CWgradMixed(ctypes.Structure):
@@ -512,7 +513,7 @@ def ep_grouped_swiglu_backward(dy: torch.Tensor, dy_scale: torch.Tensor, down: t
                                rows_div: int = 1, weights: Optional[torch.Tensor] = None,
                                pos: Optional[torch.Tensor] = None, weights_dtype: torch.dtype = torch.float32,
                                layout: Optional[Layout] = None, slot_down=None, slot_down_scale=None, grad=None, q=None,
-                               q_scale=None, grad_weights=None, ws=None, stream=None):
+                               q_scale=None, grad_weights=None, ws=None, stream=None, sums8: bool = False):
     """The gradient of ep_grouped_swiglu, from the gradient of the block's output and what was kept.
 
     dy, dy_scale: the output's gradient, a row for each token, from ep_quant_rows; down [G][I][columns of dy] and its
@@ -520,7 +521,7 @@ def ep_grouped_swiglu_backward(dy: torch.Tensor, dy_scale: torch.Tensor, down: t
     Returns (grad bf16 [M][2 I], the dy of the projections' weight gradient; q and q_scale, the same in 8 bits
     [M][2 * (I up to 128)], the x of the grouped product that gives the input gradient; grad_weights).  grad_weights,
     where weights are given: in weights_dtype, float32 or bfloat16, by pair where pos (int32, each pair's position)
-    is given, else by position; from the 8-bit product, whose sums keep about 16 bits."""
+    is given, else by position.  sums8: as there."""
     if dy.dim() != 2 or down.dim() != 3 or dy.shape[1] % 128 or dy.shape[1] != down.shape[2]:
         raise EPBalanceError(f"dy [rows][k] and down [groups][inter][k] must share k, a multiple of 128: got "
                              f"{tuple(dy.shape)} and {tuple(down.shape)}")
@@ -546,6 +547,7 @@ def ep_grouped_swiglu_backward(dy: torch.Tensor, dy_scale: torch.Tensor, down: t
                          _matrix(down, down_scale, I, K, "down"), _CMatrix(), None, None, 0,
                          EP_DTYPE_FP8 if fp8 else EP_DTYPE_BF16, kept.data_ptr(),
                          kept_scale.data_ptr() if fp8 else None, grad.data_ptr(), q.data_ptr(), q_scale.data_ptr())
+    p.sums8 = int(bool(sums8))
     if weights is not None:
         p.weights_count = _pair_weights(weights, None if rows is not None else M)
         pairs = M if pos is None else _places(pos, "pos")
@@ -734,7 +736,7 @@ def run_layer_train(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layou
 
     What is kept of the activations for it: x and the weighted silu(g) u in 8 bits, as the products take them, and g
     and u in `keep` (torch.float8_e4m3fn or torch.bfloat16).  experts and slots need gate and up with their own scales
-    (ExpertRows).  sums8: as in ep_grouped_swiglu."""
+    (ExpertRows).  sums8: as in ep_grouped_swiglu, here and in the backward pass."""
     if x.dim() != 2 or logits.dim() != 2 or x.shape[0] != logits.shape[0]:
         raise EPBalanceError(f"x [tokens][hidden] and logits [tokens][experts] must have the same tokens, got "
                              f"{tuple(x.shape)} and {tuple(logits.shape)}")
@@ -757,7 +759,7 @@ def run_layer_train(x: torch.Tensor, logits: torch.Tensor, k: int, layout: Layou
     out = ep_moe_combine(y, pos.view(-1, k), torch.ones_like(weights))
     return dict(out=out, ids=ids, weights=weights, plan=plan, status=status, offsets=offsets[0], pos=pos[0], src=src[0],
                 x=(xq, xs), h=(h, hs), kept=(kept, ks), top_k=k, scale=scale, logits_dtype=logits.dtype,
-                hidden=x.shape[1], inter=experts.inter)
+                hidden=x.shape[1], inter=experts.inter, sums8=sums8)
 
 
 def run_layer_backward(kept: dict, grad_out: torch.Tensor, layout: Layout, experts: ExpertBackwardRows,
@@ -781,7 +783,7 @@ def run_layer_backward(kept: dict, grad_out: torch.Tensor, layout: Layout, exper
     grad, q, qs, dw = ep_grouped_swiglu_backward(
         dq, ds, experts.down_t, experts.down_t_scale, *kept["kept"], offsets, rows=src, rows_div=k,
         weights=weights.view(-1), pos=pos, layout=layout, slot_down=slots.down_t if spare else None,
-        slot_down_scale=slots.down_t_scale if spare else None)
+        slot_down_scale=slots.down_t_scale if spare else None, sums8=kept["sums8"])
     dx = ep_grouped_matmul(q, qs, experts.both_t, experts.both_t_scale, offsets, layout=layout,
                            slot_w=slots.both_t if spare else None,
                            slot_w_scale=slots.both_t_scale if spare else None)
