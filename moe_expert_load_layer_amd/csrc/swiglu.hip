@@ -97,10 +97,11 @@ __device__ __forceinline__ float other_half_sum(float v) {
     return __builtin_bit_cast(float, t.a) + __builtin_bit_cast(float, t.b);
 }
 
-// The largest magnitude for a block's scale, in two steps: over all values (NaN is
-// passed over), and, only where that is infinity, over the finite ones alone.
-__device__ __forceinline__ float largest(float m, float a, float b) { return fmaxf(fmaxf(m, fabsf(a)), fabsf(b)); }
-__device__ __forceinline__ float finite(float m, float v) { return fmaxf(m, fmaf(v, 0.0f, fabsf(v))); }  // infinity * 0 is NaN
+// The largest finite magnitude, for a block's scale: infinity times 0 is NaN, which a
+// maximum passes over.  (One instruction a value; a second look at the values of rows that
+// hold infinities needs the registers that their sums leave: 12 % of the backward kernel.)
+__device__ __forceinline__ float finite(float v) { return fmaf(v, 0.0f, fabsf(v)); }
+__device__ __forceinline__ float largest(float m, float a, float b) { return fmaxf(fmaxf(m, finite(a)), finite(b)); }
 
 // The upper halves of two floats with the lowest bit set: rounding these 8 bits of
 // mantissa to the 4 of 8-bit floating point then gives what rounding the floats
@@ -112,17 +113,6 @@ __device__ __forceinline__ uint32_t odd_pair(float a, float b) {
                  0x00010001u;
     asm volatile("" : "+v"(v));  // one register, not the two that it could be made of again
     return v;
-}
-
-// The largest finite magnitude of odd pairs, for rows that hold infinities.
-template <int kCount>
-__device__ __forceinline__ float largest_finite(const uint32_t (&v)[kCount][8]) {
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kCount; i++)
-#pragma unroll
-        for (int e = 0; e < 8; e++) m = finite(finite(m, bf16_lo(v[i][e])), bf16_hi(v[i][e]));
-    return m;
 }
 
 // 8-bit values of floats, or of odd pairs, over a block's scale: the hardware's
@@ -271,22 +261,11 @@ struct GatedTile {
         shared.full[buf][thread / kWave] = __all(place >= 0);
     }
 
-    // where a row of g or u has infinities
-    template <int F>
-    __device__ __forceinline__ static float largest_finite_of(const f32x16 *const (&v)[F]) {
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < F; i++)
-#pragma unroll
-            for (int e = 0; e < 16; e++) m = finite(m, (*v[i])[e]);
-        return m;
-    }
     // h of the wave's columns of a row, and the scale bytes that they need by themselves:
     // of h, and of g and u where those are kept in 8 bits
     template <int F>
     __device__ __forceinline__ static uint32_t activate(const f32x16 *const (&g)[F], const f32x16 *const (&u)[F],
                                                         float weight, uint32_t (&h)[F][8]) {
-        const float inf = __builtin_inff();
         float th = 0, tg = 0, tu = 0;
 #pragma unroll
         for (int i = 0; i < F; i++)
@@ -314,11 +293,8 @@ struct GatedTile {
                     now(tu);
                 }
             }
-        if (__any(th == inf)) th = largest_finite(h);
         uint32_t code = fp8_scale_code(other_half_max(th));
         if constexpr (kKeep == kEight) {
-            if (__any(tg == inf)) tg = largest_finite_of(g);
-            if (__any(tu == inf)) tu = largest_finite_of(u);
             code |= fp8_scale_code(other_half_max(tg)) << 8 | fp8_scale_code(other_half_max(tu)) << 16;
         }
         return code;
@@ -645,9 +621,6 @@ struct GatedBackTile {
             uint32_t vg[FN][8], vu[FN][8];
             differentiate(B, W, R, d, c0, A.N, l, vg, vu);
             if (B.q) {
-                const float inf = __builtin_inff();
-                if (__any(R.tg == inf)) R.tg = largest_finite(vg);
-                if (__any(R.tu == inf)) R.tu = largest_finite(vu);
                 const int cg = fp8_scale_code(other_half_max(R.tg)), cu = fp8_scale_code(other_half_max(R.tu));
                 settle(vg, cg);
                 settle(vu, cu);
