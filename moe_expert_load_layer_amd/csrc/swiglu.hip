@@ -813,7 +813,7 @@ extern "C" int ep_grouped_swiglu_backward(const ep_grouped_swiglu_backward_t *p,
                              p->inter, p->k, p->weights, p->weights_count};
     if (!product_sizes_ok(shape) || !keep_dtype(p->keep_dtype) || (p->sums8 != 0 && p->sums8 != 1))
         return EP_ERR_INVALID_ARG;
-    if (p->grad_weights && (!float_dtype(p->grad_weights_dtype) || p->pairs < 0 || p->pairs > (int64_t)1 << 38 ||
+    if (p->grad_weights && (!float_dtype(p->grad_weights_dtype) || p->pairs < 0 || p->pairs > kMaxBlocks * kDotThreads ||
                             !is_aligned(p->grad_weights, p->grad_weights_dtype == EP_DTYPE_BF16 ? 2 : 4) ||
                             !is_aligned(p->pos, 4) || (!p->pos && p->pairs != p->m)))
         return EP_ERR_INVALID_ARG;
@@ -842,7 +842,6 @@ extern "C" int ep_grouped_swiglu_backward(const ep_grouped_swiglu_backward_t *p,
     }
     if (p->grad_weights && p->pairs > 0) {
         const int64_t blocks = ceil_div(p->pairs, kDotThreads);
-        if (blocks > kMaxBlocks) return EP_ERR_INVALID_ARG;
         const int ib = (int)ceil_div(p->inter, kScaleBlock);
         auto run = [&](auto kernel) {
             kernel<<<(uint32_t)blocks, kDotThreads, 0, to_stream(stream)>>>(static_cast<const float *>(p->ws), ib, p->m,
