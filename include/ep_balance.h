@@ -531,8 +531,10 @@ int ep_grouped_wgrad(const ep_grouped_wgrad_t *p, ep_stream_t stream);
  *   x, x_scale  rows of k values in 8 bits, x_rows of them; x_rows >= m without x_places
  *   dy_places, x_places  device int32 [m] or NULL
  *   ws       ep_wgrad_mixed_workspace_bytes(x_rows, k) bytes, 16-byte aligned: x in
- *            bf16, which holds its values exactly; no state between calls, calls in
- *            flight at once need their own
+ *            bf16, twice its bytes; no state between calls, calls in flight at once
+ *            need their own.  bf16 holds x's values under scale bytes from 3 to 246
+ *            exactly; under smaller ones those below 2^-133 are rounded to multiples of
+ *            it, under larger ones those from 2^128 on are infinite
  */
 typedef struct ep_grouped_wgrad_mixed {
     const void *dy;
@@ -580,7 +582,10 @@ int ep_grouped_wgrad_mixed(const ep_grouped_wgrad_mixed_t *p, ep_stream_t stream
  *            ep_grouped_matmul, in little more than half the time for many rows; they
  *            are off by up to 6e-5 of a result where some columns of x are much larger
  *            than others, and send one value in 300 the other way, by a sixteenth of it
- * A row's outputs do not depend on the other rows.
+ * A row's outputs do not depend on the other rows.  With sums8 = 0 both operands are
+ * taken in bf16, which holds their values under scale bytes from 3 to 246 exactly; under
+ * smaller ones those below 2^-133 are rounded to multiples of it, under larger ones
+ * those from 2^128 on are infinite.
  */
 typedef struct ep_grouped_swiglu {
     const void *x;

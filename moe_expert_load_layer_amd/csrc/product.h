@@ -93,7 +93,8 @@ __device__ __forceinline__ constexpr int frag_row(int wn, int i) {
 }
 
 // The same bytes under their scale as bf16, which holds e4m3 times a power of two
-// exactly.  A lane's 32 are consecutive in K; the 16-bit instruction sums over 8 of
+// exactly for scale bytes from 3 (least value 2^-9 2^-124, bf16's own least) to 246 (448
+// 2^119 is below 2^128).  A lane's 32 are consecutive in K; the 16-bit instruction sums over 8 of
 // them (and over the 8 of the lane in the other half) at a time, in both operands alike.
 __device__ __forceinline__ void open_frag(const i32x8 &f, int code, bf16x8 (&v)[4]) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

@@ -351,8 +351,8 @@ hipError_t launch(WgradArgs &A, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Rows in 8 bits as bf16, which holds e4m3 times a power of two exactly.  A unit is one
-// row's block: 8 lanes of 16 values.
+// Rows in 8 bits as bf16, which holds e4m3 times a power of two exactly for scale bytes
+// from 3 to 246 (product.h).  A unit is one row's block: 8 lanes of 16 values.
 constexpr int kWidenThreads = 256;
 __device__ __forceinline__ u32x4 widen(uint32_t lo, uint32_t hi, float scale) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
