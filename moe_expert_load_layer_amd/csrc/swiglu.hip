@@ -13,12 +13,11 @@
 // TFLOP at 1.28 PFLOP/s by the 16-bit instruction, which bounds it; with g and u kept in 8
 // bits 1770), with the 8-bit sums 943 (two plain products of these sizes 1013; 2.33 PFLOP/s,
 // bound as they are, by waiting in step; 1016), backward 1214 and 820 (one plain product
-// 500).  With those the backward kernel needs 576 for d and the
-// arithmetic, and 805 MB more of HBM traffic than the product (bf16 and 8-bit gradients out,
-// g and u in), which comes in bursts at a tile's end while no wave multiplies: one
-// workgroup a CU has all registers.  Two of 128 x 128, which could take turns, load their
-// operands twice as often and need 952; starting workgroups apart and stores that pass the
-// caches by gained nothing.
+// 500).  With 8-bit sums the backward kernel needs 576 for d and the arithmetic, and 805 MB
+// more of HBM traffic than the product (bf16 and 8-bit gradients out, g and u in), which
+// comes in bursts at a tile's end while no wave multiplies: one workgroup a CU has all
+// registers.  Two of 128 x 128, which take turns, load their operands twice as often and
+// need 952; starting workgroups apart and stores that pass the caches by gained nothing.
 #include <utility>
 
 #include "product.h"
@@ -688,14 +687,14 @@ __global__ __launch_bounds__(kDotThreads) void pair_dots_kernel(const float *__r
 // Error of the block's output y against 64 bits, exact and 8-bit sums: 65536 rows, 4096 x
 // 2048 1.66e-3 (what its rounding to bf16 gives) and 2.5e-3, 3001 rows, 1000 x 777 1.66e-3
 // and 2.0 to 3.0e-3 over four seeds (up to 9e-3 seen).  us for 8 groups of hidden 4096,
-// inter 2048, exact and 8-bit: 8192 rows a group 1720 and 990 (1.28 PFLOP/s of a library
-// product's 1.19 to 1.54 in bf16), 1000 rows 283 and 155, 400 rows 110 and 62, 100 rows 39
-// and 32, one row 35 and 28.
+// inter 2048, exact and 8-bit: 8192 rows a group 1720 and 940 to 990 (1.28 PFLOP/s; a library
+// product in bf16 has 1.19 under load, 1.54 in a short run), 1000 rows 283 and 155, 400 rows
+// 110 and 62, 100 rows 39 and 32, one row 35 and 28.
 //
 // The backward kernel the same, since its gradients are rounded to 8 bits again and dw adds
-// up terms that cancel.  Error of the input gradient formed from q 1.66e-3 and 1.9e-3
-// (with the same g and u), 820 us with the 8-bit sums for 8192 rows a group, 1214 with these;
-// 1000 rows 167 and 142, 400 rows 78 and 59, 100 rows 46 and 32.
+// up terms that cancel.  Error of the input gradient formed from q, with the same g and u:
+// 1.66e-3 and 1.9e-3.  us, exact and 8-bit: 8192 rows a group 1214 and 820, 1000 rows 167 and
+// 130, 400 rows 78 and 59, 100 rows 46 and 32.
 template <Keep kKeep, bool kExact>
 hipError_t forward(const ProductArgs &A, const typename GatedTile<kNone>::Args &B, hipStream_t s) {
     typedef GatedTile<kKeep> Tile;
